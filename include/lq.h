@@ -447,6 +447,121 @@ lq_status lq_quant_weight_block128(const void *w, void *q, float *scales,
                                    int64_t N, int64_t K, lq_stream_t stream);
 
 /*
+ * 4-bit weights: two codes per byte with a bf16 scale, and optionally a zero
+ * point, per group of `group` consecutive weights of a row (a weight-only
+ * format beside the blog's three 8-bit ones, for decode, where the weight's
+ * bytes bound a linear layer; no page defines it).
+ *
+ *   weight[n, k] = (q[n, k] - z[n, k / group]) * s[n, k / group]
+ *
+ *   q      : codes 0..15, packed [N, K / 2]: byte [n, k / 2] holds the even k
+ *            in its low half and the odd k in its high half.
+ *   scales : [N, K / group] bf16.
+ *   zeros  : [N, K / group] bytes, 0..15 (the low four bits are used), or
+ *            NULL: every zero point is 8.
+ *   group  : 32, 64 or 128.
+ *
+ * lq_quant_weight_int4 quantizes a bf16 weight w [N, K] (16-byte aligned;
+ * q 4-byte aligned; finite values).  zeros == NULL, symmetric:
+ *   s = max(bf16(amax / 7), 2^-126), q = clamp(rint(w / s), -8, 7) + 8;
+ * else, with lo = min(0, min w) and hi = max(0, max w) of the group:
+ *   s = max(bf16((hi - lo) / 15), 2^-126), z = clamp(rint(-lo / s), 0, 15),
+ *   q = clamp(rint(w / s) + z, 0, 15).
+ * Differences and quotients are rounded to fp32 and rint rounds half to even,
+ * so codes, scales and zero points are reproducible bit for bit.
+ * K % group == 0.  N == 0 or K == 0 is a no-op.
+ * Errors as lq_quant_weight_block128; LQ_ERR_INVALID_ARG for another group.
+ */
+lq_status lq_quant_weight_int4(const void *w, int64_t group, void *q, void *scales,
+                               void *zeros, int64_t N, int64_t K, lq_stream_t stream);
+
+/*
+ * Product with 4-bit weights: C[m, n] = bf16(sum_k x[m, k] weight[n, k]
+ * [+ bias[n]]), sums in fp32.
+ *
+ *   x        : [M, K] bf16 activations, 16-byte aligned.
+ *   B        : [N, K / 2] packed codes, 16-byte aligned; b_scales, b_zeros
+ *              (or NULL) as above.
+ *   bias     : [N] bf16 or NULL, added in fp32 before the rounding.
+ *   C        : [M, N] bf16 out, 16-byte aligned.
+ *   K        : a positive multiple of group; N % 8 == 0.  M == 0 or N == 0 is
+ *              a no-op.
+ * The codes minus the zero points are exact in bf16, a group's products are
+ * summed in fp32 and then multiplied by the group's scale in fp32.
+ * Errors: LQ_ERR_INVALID_ARG, LQ_ERR_ALIGNMENT, LQ_ERR_UNSUPPORTED_SHAPE
+ * before any launch; LQ_ERR_CUDA.
+ */
+lq_status lq_int4_mm(const void *x, const void *B, const void *b_scales,
+                     const void *b_zeros, const void *bias, void *C, int64_t M,
+                     int64_t N, int64_t K, int64_t group, lq_stream_t stream);
+
+/*
+ * Grouped (mixture-of-experts) product with 4-bit weights: x [T, K] sorted by
+ * expert, B [E, N, K / 2], b_scales and b_zeros [E, N, K / group], C [T, N].
+ * expert_offsets as for lq_grouped_scaled_mm (clamped to [0, T] and to their
+ * running maximum); rows of C outside every expert are left as they were.
+ * E * N < 2^31.  Errors as lq_int4_mm; LQ_ERR_INVALID_ARG for E = 0 with T > 0.
+ */
+lq_status lq_grouped_int4_mm(const void *x, const void *B, const void *b_scales,
+                             const void *b_zeros, void *C, const int32_t *expert_offsets,
+                             int64_t E, int64_t T, int64_t N, int64_t K, int64_t group,
+                             lq_stream_t stream);
+
+/*
+ * Mixture-of-experts token movement around the grouped products (their expert
+ * offsets and row order; ai-radar.it, "Helion in vLLM: il tuning dei GEMM
+ * diventa ricerca, non artigianato GPU", section "Oltre Hopper: Blackwell, AMD,
+ * TPU e il perimetro del fork", names the expert products only).
+ *
+ * lq_moe_sort: the rows of all (token, choice) pairs sorted by expert, stably.
+ *   ids    : [n] expert ids, n = tokens * k, int32 (id_bytes 4) or int64 (8).
+ *            An id outside [0, E) (-1: not routed here) takes no row.
+ *   expert_offsets : [E + 1] out: expert e's rows are expert_offsets[e] ..
+ *            expert_offsets[e + 1] - 1, as the grouped products read them.
+ *   order  : [n] out: order[p] = i, the pair of row p; -1 behind the last row.
+ *   slots  : [n] out: slots[i] = p, the row of pair i, or -1.
+ *   1 <= E <= 1024, n < 2^31.  n == 0 writes zero offsets.  One launch; no
+ *   workspace, no atomics.
+ *
+ * In the calls below T tokens have k slots each (slots [T, k], from
+ * lq_moe_sort), P is the number of rows of the sorted arrays (T * k, or fewer
+ * when the caller knows a bound), and a slot outside [0, P) is skipped: its
+ * row is neither read nor written.  Rows that no slot names are left as they
+ * were.  Slots that name a row twice give that row one of the two values.
+ * Outputs must not overlap inputs.  H % 8 == 0 (lq_moe_permute_quant: 16), H <= 2^25; rows
+ * are dense and 16-byte aligned (codes 8).
+ *
+ * lq_moe_permute: xs[slots[t, j]] = x[t]; x [T, H] bf16, xs [P, H] bf16.  Its
+ *   gradient is lq_moe_unpermute with weights NULL.
+ * lq_moe_permute_quant: the same with each row quantized as
+ *   lq_quant_per_token would: q [P, H] codes, scales [P] fp32.
+ * lq_moe_unpermute: out[t] = bf16(sum_j weights[t, j] y[slots[t, j]]), summed
+ *   in fp32 in the order of j; weights [T, k] fp32, or NULL for ones.  A
+ *   token without rows gets zeros.
+ * lq_moe_unpermute_backward: the gradients of lq_moe_unpermute from dout
+ *   [T, H] bf16: dy[slots[t, j]] = bf16(weights[t, j] dout[t]) (dy [P, H]) and
+ *   dweights[t, j] = sum_h dout[t, h] y[slots[t, j], h] in fp32 ([T, k]; 0 for a
+ *   skipped slot).
+ * Errors: LQ_ERR_INVALID_ARG, LQ_ERR_ALIGNMENT, LQ_ERR_UNSUPPORTED_SHAPE
+ * before any launch; LQ_ERR_CUDA.
+ */
+lq_status lq_moe_sort(const void *ids, int64_t id_bytes, int64_t n, int64_t E,
+                      int32_t *expert_offsets, int32_t *order, int32_t *slots,
+                      lq_stream_t stream);
+lq_status lq_moe_permute(const void *x, const int32_t *slots, void *xs, int64_t T,
+                         int64_t P, int64_t k, int64_t H, lq_stream_t stream);
+lq_status lq_moe_permute_quant(lq_fmt fmt, const void *x, const int32_t *slots, void *q,
+                               float *scales, int64_t T, int64_t P, int64_t k, int64_t H,
+                               lq_stream_t stream);
+lq_status lq_moe_unpermute(const void *y, const int32_t *slots, const float *weights,
+                           void *out, int64_t T, int64_t P, int64_t k, int64_t H,
+                           lq_stream_t stream);
+lq_status lq_moe_unpermute_backward(const void *dout, const void *y, const int32_t *slots,
+                                    const float *weights, void *dy, float *dweights,
+                                    int64_t T, int64_t P, int64_t k, int64_t H,
+                                    lq_stream_t stream);
+
+/*
  * The variant that lq_scaled_mm uses for (fmt, M, N, K) when given NULL:
  * the dispatch-table entry for the token bucket of M (the next of
  * 1,2,4,8,16,24,32, then powers of two), else a built-in heuristic.

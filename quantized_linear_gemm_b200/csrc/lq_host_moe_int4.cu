@@ -1,0 +1,150 @@
+// Entry points of the 4-bit weight products and of the mixture-of-experts
+// token movement: argument checks, then one launch each (include/lq.h).
+#include <cuda_runtime.h>
+#include <cstdint>
+
+#include "../../include/lq.h"
+#include "lq_kernels.h"
+
+namespace {
+
+constexpr int64_t kMaxInt = 0x7FFFFFFF;
+
+bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+lq_status launched(cudaError_t e) {
+  if (e == cudaSuccess) return LQ_OK;
+  cudaGetLastError();
+  return LQ_ERR_CUDA;
+}
+
+bool group_ok(int64_t group) { return group == 32 || group == 64 || group == 128; }
+
+// Shared by the dense (E = 1) and grouped products.
+lq_status int4_mm_impl(const void* x, const void* B, const void* scales, const void* zeros, const void* bias, void* C,
+                       const int32_t* offsets, bool grouped, int64_t E, int64_t M, int64_t N, int64_t K,
+                       int64_t group, lq_stream_t stream_) {
+  const cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+  if (M < 0 || N < 0 || K < 0 || E < 0 || !group_ok(group)) return LQ_ERR_INVALID_ARG;
+  if (M == 0 || N == 0) return LQ_OK;
+  if (!C || (grouped && (E == 0 || !offsets))) return LQ_ERR_INVALID_ARG;
+  if (!x || !B || !scales) return LQ_ERR_INVALID_ARG;
+  if (!aligned(C, 16) || !aligned(x, 16) || !aligned(B, 16) || !aligned(scales, 2) || (bias && !aligned(bias, 2)) ||
+      (offsets && !aligned(offsets, 4)))
+    return LQ_ERR_ALIGNMENT;
+  if (K == 0 || K % group != 0 || N % 8 != 0) return LQ_ERR_UNSUPPORTED_SHAPE;
+  if (M > kMaxInt || K > kMaxInt || E > kMaxInt || N > kMaxInt || E * N > kMaxInt) return LQ_ERR_UNSUPPORTED_SHAPE;
+  lq::Int4Params p{};
+  p.x = static_cast<const __nv_bfloat16*>(x);
+  p.B = static_cast<const uint8_t*>(B);
+  p.scales = static_cast<const __nv_bfloat16*>(scales);
+  p.zeros = static_cast<const uint8_t*>(zeros);
+  p.bias = static_cast<const __nv_bfloat16*>(bias);
+  p.C = static_cast<__nv_bfloat16*>(C);
+  p.M = M;
+  p.N = N;
+  p.K = K;
+  p.expert_offsets = grouped ? offsets : nullptr;
+  p.num_experts = static_cast<int>(E);
+  const int64_t tiles = (M + 15) / 16 + (grouped ? (E < M ? E : M) : 0);   // token tiles, the grid's y
+  if (M > 8 && tiles > 65535) return LQ_ERR_UNSUPPORTED_SHAPE;
+  return launched(lq::launch_int4_mm(p, static_cast<int>(group), stream));
+}
+
+// Shared checks of the row movements: T tokens of k slots, rows of H values.
+lq_status check_rows(int64_t T, int64_t P, int64_t k, int64_t H, int64_t multiple) {
+  if (T < 0 || P < 0 || k < 0 || H < 0) return LQ_ERR_INVALID_ARG;
+  if (H % multiple != 0 || T > kMaxInt || k > kMaxInt || P > kMaxInt || H > (int64_t(1) << 25))
+    return LQ_ERR_UNSUPPORTED_SHAPE;
+  return LQ_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+lq_status lq_quant_weight_int4(const void* w, int64_t group, void* q, void* scales, void* zeros, int64_t N, int64_t K,
+                               lq_stream_t stream) {
+  if (N < 0 || K < 0 || !group_ok(group)) return LQ_ERR_INVALID_ARG;
+  if (N == 0 || K == 0) return LQ_OK;
+  if (!w || !q || !scales) return LQ_ERR_INVALID_ARG;
+  if (!aligned(w, 16) || !aligned(q, 4) || !aligned(scales, 2)) return LQ_ERR_ALIGNMENT;
+  if (K % group != 0 || K > kMaxInt || N > kMaxInt || (N * K / 8 + 255) / 256 > kMaxInt)
+    return LQ_ERR_UNSUPPORTED_SHAPE;
+  return launched(lq::launch_quant_weight_int4(w, static_cast<int>(group), q, scales, zeros, N, K,
+                                               reinterpret_cast<cudaStream_t>(stream)));
+}
+
+lq_status lq_int4_mm(const void* x, const void* B, const void* b_scales, const void* b_zeros, const void* bias,
+                     void* C, int64_t M, int64_t N, int64_t K, int64_t group, lq_stream_t stream) {
+  return int4_mm_impl(x, B, b_scales, b_zeros, bias, C, nullptr, false, 1, M, N, K, group, stream);
+}
+
+lq_status lq_grouped_int4_mm(const void* x, const void* B, const void* b_scales, const void* b_zeros, void* C,
+                             const int32_t* expert_offsets, int64_t E, int64_t T, int64_t N, int64_t K, int64_t group,
+                             lq_stream_t stream) {
+  return int4_mm_impl(x, B, b_scales, b_zeros, nullptr, C, expert_offsets, true, E, T, N, K, group, stream);
+}
+
+lq_status lq_moe_sort(const void* ids, int64_t id_bytes, int64_t n, int64_t E, int32_t* expert_offsets,
+                      int32_t* order, int32_t* slots, lq_stream_t stream) {
+  if (n < 0 || E < 0 || (id_bytes != 4 && id_bytes != 8)) return LQ_ERR_INVALID_ARG;
+  if (!expert_offsets || (n > 0 && (!ids || !order || !slots))) return LQ_ERR_INVALID_ARG;
+  if (!aligned(ids, static_cast<uintptr_t>(id_bytes)) || !aligned(expert_offsets, 4) || !aligned(order, 4) ||
+      !aligned(slots, 4))
+    return LQ_ERR_ALIGNMENT;
+  if (E == 0 || E > lq::moe_sort_max_experts() || n > kMaxInt) return LQ_ERR_UNSUPPORTED_SHAPE;
+  return launched(lq::launch_moe_sort(ids, static_cast<int>(id_bytes), n, static_cast<int>(E), expert_offsets, order,
+                                      slots, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+lq_status lq_moe_permute(const void* x, const int32_t* slots, void* xs, int64_t T, int64_t P, int64_t k, int64_t H,
+                         lq_stream_t stream) {
+  const lq_status rc = check_rows(T, P, k, H, 8);
+  if (rc != LQ_OK) return rc;
+  if (T == 0 || P == 0 || k == 0 || H == 0) return LQ_OK;
+  if (!x || !slots || !xs) return LQ_ERR_INVALID_ARG;
+  if (!aligned(x, 16) || !aligned(xs, 16) || !aligned(slots, 4)) return LQ_ERR_ALIGNMENT;
+  return launched(lq::launch_moe_permute(x, slots, xs, T, P, static_cast<int>(k), H,
+                                         reinterpret_cast<cudaStream_t>(stream)));
+}
+
+lq_status lq_moe_permute_quant(lq_fmt fmt, const void* x, const int32_t* slots, void* q, float* scales, int64_t T,
+                               int64_t P, int64_t k, int64_t H, lq_stream_t stream) {
+  if (fmt != LQ_FP8_DYNAMIC && fmt != LQ_W8A8_INT8) return LQ_ERR_INVALID_ARG;
+  const lq_status rc = check_rows(T, P, k, H, 16);
+  if (rc != LQ_OK) return rc;
+  if (T == 0 || P == 0 || k == 0) return LQ_OK;
+  if (!x || !slots || !q || !scales) return LQ_ERR_INVALID_ARG;
+  if (!aligned(x, 16) || !aligned(q, 8) || !aligned(scales, 4) || !aligned(slots, 4)) return LQ_ERR_ALIGNMENT;
+  return launched(lq::launch_moe_permute_quant(static_cast<int>(fmt), x, slots, q, scales, T, P, static_cast<int>(k),
+                                               H, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+lq_status lq_moe_unpermute(const void* y, const int32_t* slots, const float* weights, void* out, int64_t T, int64_t P,
+                           int64_t k, int64_t H, lq_stream_t stream) {
+  const lq_status rc = check_rows(T, P, k, H, 8);
+  if (rc != LQ_OK) return rc;
+  if (T == 0 || H == 0) return LQ_OK;
+  if (!out || (k > 0 && !slots) || (k > 0 && P > 0 && !y)) return LQ_ERR_INVALID_ARG;
+  if (!aligned(y, 16) || !aligned(out, 16) || !aligned(slots, 4) || !aligned(weights, 4)) return LQ_ERR_ALIGNMENT;
+  return launched(lq::launch_moe_unpermute(y, slots, weights, out, T, P, static_cast<int>(k), H,
+                                           reinterpret_cast<cudaStream_t>(stream)));
+}
+
+lq_status lq_moe_unpermute_backward(const void* dout, const void* y, const int32_t* slots, const float* weights,
+                                    void* dy, float* dweights, int64_t T, int64_t P, int64_t k, int64_t H,
+                                    lq_stream_t stream) {
+  const lq_status rc = check_rows(T, P, k, H, 8);
+  if (rc != LQ_OK) return rc;
+  if (T == 0 || k == 0) return LQ_OK;
+  if (!slots || !weights || !dweights) return LQ_ERR_INVALID_ARG;
+  if (H > 0 && (!dout || (P > 0 && (!y || !dy)))) return LQ_ERR_INVALID_ARG;
+  if (!aligned(dout, 16) || !aligned(y, 16) || !aligned(dy, 16) || !aligned(slots, 4) || !aligned(weights, 4) ||
+      !aligned(dweights, 4))
+    return LQ_ERR_ALIGNMENT;
+  return launched(lq::launch_moe_unpermute_backward(dout, y, slots, weights, dy, dweights, T, P, static_cast<int>(k),
+                                                    H, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"

@@ -108,4 +108,36 @@ cudaError_t launch_quant_weight_block128(const void* w, void* q, void* scales, i
                                          cudaStream_t stream);
 cudaError_t launch_fill_zero_bf16(__nv_bfloat16* C, int64_t count, cudaStream_t stream);
 
+// Products with 4-bit weights (int4_kernels.cu): x [M, K] bf16, B [N, K / 2]
+// packed codes, scales (and zeros, or null) [N, K / group].
+struct Int4Params {
+  const __nv_bfloat16* x;
+  const uint8_t* B;
+  const __nv_bfloat16* scales;
+  const uint8_t* zeros;        // null: every zero point is 8
+  const __nv_bfloat16* bias;   // optional [N]
+  __nv_bfloat16* C;
+  int64_t M, N, K;
+  const int* expert_offsets;   // grouped: device [num_experts + 1], N rows of B per expert; null = one product
+  int num_experts;
+};
+cudaError_t launch_int4_mm(const Int4Params& p, int group, cudaStream_t stream);
+cudaError_t launch_quant_weight_int4(const void* w, int group, void* q, void* scales, void* zeros, int64_t N,
+                                     int64_t K, cudaStream_t stream);
+
+// Mixture-of-experts token movement (moe_kernels.cu): T tokens, k slots per
+// token, P rows sorted by expert, H values per row.
+int moe_sort_max_experts();
+cudaError_t launch_moe_sort(const void* ids, int id_bytes, int64_t n, int E, int32_t* offsets, int32_t* order,
+                            int32_t* slots, cudaStream_t stream);
+cudaError_t launch_moe_permute(const void* x, const int32_t* slots, void* xs, int64_t T, int64_t P, int k, int64_t H,
+                               cudaStream_t stream);
+cudaError_t launch_moe_permute_quant(int fmt, const void* x, const int32_t* slots, void* q, float* scales, int64_t T,
+                                     int64_t P, int k, int64_t H, cudaStream_t stream);
+cudaError_t launch_moe_unpermute(const void* y, const int32_t* slots, const float* weights, void* out, int64_t T,
+                                 int64_t P, int k, int64_t H, cudaStream_t stream);
+cudaError_t launch_moe_unpermute_backward(const void* dout, const void* y, const int32_t* slots, const float* weights,
+                                          void* dy, float* dweights, int64_t T, int64_t P, int k, int64_t H,
+                                          cudaStream_t stream);
+
 }  // namespace lq

@@ -41,7 +41,8 @@ EXPORTED = (
     "lq_quant_scaled_mm", "lq_set_fuse_limit", "lq_rms_norm_dynamic_per_token_quant",
     "lq_rms_norm_per_block_quant", "lq_silu_and_mul_dynamic_per_token_quant", "lq_silu_and_mul_per_block_quant",
     "lq_grouped_scaled_mm", "lq_quant_per_token_group128_ue8m0", "lq_quant_weight_block128_ue8m0",
-    "lq_scaled_mm_bias", "lq_declare_static_weights",
+    "lq_scaled_mm_bias", "lq_declare_static_weights", "lq_quant_weight_int4", "lq_int4_mm", "lq_grouped_int4_mm",
+    "lq_moe_sort", "lq_moe_permute", "lq_moe_permute_quant", "lq_moe_unpermute", "lq_moe_unpermute_backward",
 )
 
 
@@ -133,6 +134,17 @@ def lib() -> ctypes.CDLL:
             L.lq_scaled_mm_bias.argtypes = [_i32, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64,
                                             ctypes.POINTER(Variant), _st]
             L.lq_scaled_mm_bias.restype = _i32
+            L.lq_quant_weight_int4.argtypes = [_vp, _i64, _vp, _vp, _vp, _i64, _i64, _st]
+            L.lq_int4_mm.argtypes = [_vp] * 6 + [_i64] * 4 + [_st]
+            L.lq_grouped_int4_mm.argtypes = [_vp] * 6 + [_i64] * 5 + [_st]
+            L.lq_moe_sort.argtypes = [_vp, _i64, _i64, _i64, _vp, _vp, _vp, _st]
+            L.lq_moe_permute.argtypes = [_vp] * 3 + [_i64] * 4 + [_st]
+            L.lq_moe_permute_quant.argtypes = [_i32] + [_vp] * 4 + [_i64] * 4 + [_st]
+            L.lq_moe_unpermute.argtypes = [_vp] * 4 + [_i64] * 4 + [_st]
+            L.lq_moe_unpermute_backward.argtypes = [_vp] * 6 + [_i64] * 4 + [_st]
+            for name in ("lq_quant_weight_int4", "lq_int4_mm", "lq_grouped_int4_mm", "lq_moe_sort", "lq_moe_permute",
+                         "lq_moe_permute_quant", "lq_moe_unpermute", "lq_moe_unpermute_backward"):
+                getattr(L, name).restype = _i32
             L.lq_version.argtypes = []
             L.lq_version.restype = ctypes.c_char_p
             for name in ("lq_scaled_mm", "lq_scaled_mm_i32acc", "lq_quant_per_token", "lq_quant_per_token_group128",
@@ -474,6 +486,206 @@ def quant_weight_block128(w: torch.Tensor, q=None, scales=None, stream=None):
     rc = lib().lq_quant_weight_block128(_ptr(w), _ptr(q), _ptr(scales), N, K, _stream(stream))
     _check("lq_quant_weight_block128", rc)
     return q, scales
+
+
+INT4_GROUPS = (32, 64, 128)
+
+
+def quant_weight_int4(w: torch.Tensor, group: int = 128, zero_points: bool = False, q=None, scales=None, zeros=None,
+                      stream=None):
+    """``lq_quant_weight_int4``: (packed codes uint8 [N, K/2], scales bf16
+    [N, K/group], zero points uint8 [N, K/group] or None) of a bf16 weight
+    [N, K]; symmetric unless ``zero_points`` (or ``zeros`` is given)."""
+    _need(w, "w", (torch.bfloat16,), 2)
+    N, K = w.shape
+    if group not in INT4_GROUPS or K % group:
+        raise ValueError(f"group must be one of {INT4_GROUPS} and divide K = {K}, got {group}")
+    q, scales = _outputs(w.device, q, (N, K // 2), torch.uint8, scales, (N, K // group), torch.bfloat16)
+    if zeros is not None:
+        _need(zeros, "zeros", (torch.uint8,), 2, (N, K // group))
+    elif zero_points:
+        zeros = torch.empty((N, K // group), dtype=torch.uint8, device=w.device)
+    _one_device(w, q, scales, zeros)
+    _check("lq_quant_weight_int4", lib().lq_quant_weight_int4(_ptr(w), group, _ptr(q), _ptr(scales), _ptr(zeros), N, K,
+                                                              _stream(stream)))
+    return q, scales, zeros
+
+
+def _int4_operands(x, B, b_scales, b_zeros, lead: tuple):
+    """Check x [M, K] and a 4-bit weight with leading dimensions `lead`
+    (() or (E,)); returns (M, N, K, group)."""
+    _need(x, "x", (torch.bfloat16,), 2)
+    _need(B, "B", (torch.uint8,), 2 + len(lead))
+    M, K = x.shape
+    N = B.shape[-2]
+    if B.shape[-1] * 2 != K:
+        raise ValueError(f"B has {B.shape[-1]} bytes per row, expected K / 2 with K = {K}")
+    _need(b_scales, "b_scales", (torch.bfloat16,), 2 + len(lead))
+    groups = b_scales.shape[-1]
+    if groups == 0 or K % groups or K // groups not in INT4_GROUPS:
+        raise ValueError(f"b_scales has {groups} groups per row: K = {K} must hold whole groups of {INT4_GROUPS}")
+    want = (*lead, N, groups)
+    if tuple(b_scales.shape) != want:
+        raise ValueError(f"b_scales has shape {tuple(b_scales.shape)}, expected {want}")
+    if b_zeros is not None:
+        _need(b_zeros, "b_zeros", (torch.uint8,), 2 + len(lead), want)
+    return M, N, K, K // groups
+
+
+def int4_mm(x: torch.Tensor, B: torch.Tensor, b_scales: torch.Tensor, b_zeros: torch.Tensor | None = None,
+            bias: torch.Tensor | None = None, C: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """``lq_int4_mm``: C [M, N] bf16 = x [M, K] bf16 times the 4-bit weight
+    (packed codes B [N, K/2], scales [N, K/group], optional zero points), plus
+    an optional bf16 bias [N].  The group size follows from the shapes."""
+    M, N, K, group = _int4_operands(x, B, b_scales, b_zeros, ())
+    if bias is not None:
+        _need(bias, "bias", (torch.bfloat16,), 1, (N,))
+    if C is None:
+        C = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
+    else:
+        _need(C, "C", (torch.bfloat16,), 2, (M, N))
+    _one_device(x, B, b_scales, b_zeros, bias, C)
+    _check("lq_int4_mm", lib().lq_int4_mm(_ptr(x), _ptr(B), _ptr(b_scales), _ptr(b_zeros), _ptr(bias), _ptr(C), M, N, K,
+                                          group, _stream(stream)))
+    return C
+
+
+def grouped_int4_mm(x: torch.Tensor, B: torch.Tensor, b_scales: torch.Tensor, expert_offsets: torch.Tensor,
+                    b_zeros: torch.Tensor | None = None, C: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """``lq_grouped_int4_mm``: x [T, K] bf16 sorted by expert, B [E, N, K/2]
+    packed codes, b_scales (and b_zeros) [E, N, K/group], expert_offsets int32
+    [E + 1] on the device.  Returns C [T, N] bf16; rows outside every expert
+    are left as they were."""
+    if not isinstance(B, torch.Tensor) or B.dim() != 3:
+        raise ValueError("B must be a contiguous 3-d tensor [E, N, K / 2]")
+    E = B.shape[0]
+    T, N, K, group = _int4_operands(x, B, b_scales, b_zeros, (E,))
+    _need(expert_offsets, "expert_offsets", (torch.int32,), 1, (E + 1,))
+    if C is None:
+        C = torch.empty((T, N), dtype=torch.bfloat16, device=x.device)
+    else:
+        _need(C, "C", (torch.bfloat16,), 2, (T, N))
+    _one_device(x, B, b_scales, b_zeros, expert_offsets, C)
+    _check("lq_grouped_int4_mm", lib().lq_grouped_int4_mm(_ptr(x), _ptr(B), _ptr(b_scales), _ptr(b_zeros), _ptr(C),
+                                                          _ptr(expert_offsets), E, T, N, K, group, _stream(stream)))
+    return C
+
+
+def moe_sort(topk_ids: torch.Tensor, num_experts: int, expert_offsets=None, order=None, slots=None, stream=None):
+    """``lq_moe_sort``: (expert_offsets int32 [E + 1], order int32 [T * k],
+    slots int32 [T, k]) of the expert ids int32 or int64 [T, k]; ids outside
+    [0, num_experts) take no row (slot -1)."""
+    _need(topk_ids, "topk_ids", (torch.int32, torch.int64), 2)
+    T, k = topk_ids.shape
+    E = int(num_experts)
+    outs = []
+    for name, t, shape in (("expert_offsets", expert_offsets, (E + 1,)), ("order", order, (T * k,)),
+                           ("slots", slots, (T, k))):
+        if t is None:
+            t = torch.empty(shape, dtype=torch.int32, device=topk_ids.device)
+        else:
+            _need(t, name, (torch.int32,), len(shape), shape)
+        outs.append(t)
+    _one_device(topk_ids, *outs)
+    _check("lq_moe_sort", lib().lq_moe_sort(_ptr(topk_ids), topk_ids.element_size(), T * k, E, *map(_ptr, outs),
+                                            _stream(stream)))
+    return tuple(outs)
+
+
+def _token_slots(slots, T: int) -> int:
+    _need(slots, "slots", (torch.int32,), 2)
+    if slots.shape[0] != T:
+        raise ValueError(f"slots has {slots.shape[0]} tokens, expected {T}")
+    return slots.shape[1]
+
+
+def moe_permute(x: torch.Tensor, slots: torch.Tensor, xs: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """``lq_moe_permute``: xs[slots[t, j]] = x[t] for bf16 x [T, H] and slots
+    int32 [T, k].  xs [P, H] (default P = T * k); rows that no slot names are
+    left as they were."""
+    _need(x, "x", (torch.bfloat16,), 2)
+    T, H = x.shape
+    k = _token_slots(slots, T)
+    if xs is None:
+        xs = torch.empty((T * k, H), dtype=torch.bfloat16, device=x.device)
+    else:
+        _need(xs, "xs", (torch.bfloat16,), 2, (xs.shape[0], H))
+    _one_device(x, slots, xs)
+    _check("lq_moe_permute", lib().lq_moe_permute(_ptr(x), _ptr(slots), _ptr(xs), T, xs.shape[0], k, H,
+                                                  _stream(stream)))
+    return xs
+
+
+def moe_permute_quant(fmt, x: torch.Tensor, slots: torch.Tensor, q: torch.Tensor | None = None,
+                      scales: torch.Tensor | None = None, stream=None):
+    """``lq_moe_permute_quant``: (codes [P, H], scales fp32 [P]) of x [T, H]
+    quantized per token (``fp8_dynamic`` or ``w8a8_int8``) and placed at its
+    slots; P = T * k unless q is given."""
+    f = _fmt(fmt)
+    _need(x, "x", (torch.bfloat16,), 2)
+    T, H = x.shape
+    k = _token_slots(slots, T)
+    if q is not None and q.dim() != 2:
+        raise ValueError("q must be a contiguous 2-d tensor")
+    P = T * k if q is None else q.shape[0]
+    q, scales = _outputs(x.device, q, (P, H), _code_dtype(f), scales, (P,))
+    _one_device(x, slots, q, scales)
+    _check("lq_moe_permute_quant", lib().lq_moe_permute_quant(f, _ptr(x), _ptr(slots), _ptr(q), _ptr(scales), T, P, k,
+                                                              H, _stream(stream)))
+    return q, scales
+
+
+def moe_unpermute(y: torch.Tensor, slots: torch.Tensor, weights: torch.Tensor | None = None,
+                  out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """``lq_moe_unpermute``: out[t] = sum_j weights[t, j] * y[slots[t, j]] for
+    bf16 y [P, H], slots int32 [T, k] and fp32 weights [T, k] (None: ones);
+    skipped slots (-1) add nothing.  Returns bf16 [T, H]."""
+    _need(y, "y", (torch.bfloat16,), 2)
+    _need(slots, "slots", (torch.int32,), 2)
+    P, H = y.shape
+    T, k = slots.shape
+    if weights is not None:
+        _need(weights, "weights", (torch.float32,), 2, (T, k))
+    if out is None:
+        out = torch.empty((T, H), dtype=torch.bfloat16, device=y.device)
+    else:
+        _need(out, "out", (torch.bfloat16,), 2, (T, H))
+    _one_device(y, slots, weights, out)
+    _check("lq_moe_unpermute", lib().lq_moe_unpermute(_ptr(y), _ptr(slots), _ptr(weights), _ptr(out), T, P, k, H,
+                                                      _stream(stream)))
+    return out
+
+
+def moe_permute_backward(dxs: torch.Tensor, slots: torch.Tensor, dx: torch.Tensor | None = None,
+                         stream=None) -> torch.Tensor:
+    """Gradient of moe_permute: dx[t] = sum_j dxs[slots[t, j]] (``lq_moe_unpermute`` without weights)."""
+    return moe_unpermute(dxs, slots, None, out=dx, stream=stream)
+
+
+def moe_unpermute_backward(dout: torch.Tensor, y: torch.Tensor, slots: torch.Tensor, weights: torch.Tensor,
+                           dy: torch.Tensor | None = None, dweights: torch.Tensor | None = None, stream=None):
+    """``lq_moe_unpermute_backward``: (dy bf16 [P, H], dweights fp32 [T, k]) of
+    moe_unpermute(y, slots, weights) for the gradient dout bf16 [T, H]; rows of
+    dy that no slot names are left as they were.  (Without weights the gradient
+    is moe_permute(dout, slots).)"""
+    _need(y, "y", (torch.bfloat16,), 2)
+    _need(slots, "slots", (torch.int32,), 2)
+    P, H = y.shape
+    T, k = slots.shape
+    _need(dout, "dout", (torch.bfloat16,), 2, (T, H))
+    _need(weights, "weights", (torch.float32,), 2, (T, k))
+    if dy is None:
+        dy = torch.empty((P, H), dtype=torch.bfloat16, device=y.device)
+    else:
+        _need(dy, "dy", (torch.bfloat16,), 2, (P, H))
+    if dweights is None:
+        dweights = torch.empty((T, k), dtype=torch.float32, device=y.device)
+    else:
+        _need(dweights, "dweights", (torch.float32,), 2, (T, k))
+    _one_device(dout, y, slots, weights, dy, dweights)
+    _check("lq_moe_unpermute_backward", lib().lq_moe_unpermute_backward(
+        _ptr(dout), _ptr(y), _ptr(slots), _ptr(weights), _ptr(dy), _ptr(dweights), T, P, k, H, _stream(stream)))
+    return dy, dweights
 
 
 def select_variant(fmt, M: int, N: int, K: int) -> Variant:

@@ -161,8 +161,13 @@ def _check(fn: str, rc: int) -> None:
 
 
 def _stream(stream=None) -> int:
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return int(s.cuda_stream)
+    """The handle of `stream`, or of torch's current stream (read directly once
+    CUDA is up: building a Stream object costs as much as a launch)."""
+    if stream is None:
+        if torch.cuda.is_initialized():
+            return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        stream = torch.cuda.current_stream()
+    return int(stream.cuda_stream)
 
 
 def _fmt(fmt) -> int:
@@ -185,19 +190,26 @@ def _need(t: torch.Tensor, name: str, dtypes, ndim: int, shape=None) -> None:
     exactly `shape` when given (the C ABI reads that many elements)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a tensor")
-    if t.device.type != _DEVICE_TYPE:
+    if not t.is_cuda if _DEVICE_TYPE == "cuda" else t.device.type != _DEVICE_TYPE:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dtype not in dtypes:
         raise TypeError(f"{name} has dtype {t.dtype}, expected one of {dtypes}")
     if t.dim() != ndim or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {ndim}-d tensor")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
 
 
 def _one_device(*ts) -> None:
     """All tensors on one device, the current CUDA device (the library
     launches on the current device and dereferences every pointer there)."""
+    index = ts[0].get_device()
+    if index >= 0 and index == torch.cuda.current_device():   # the usual case, without building device objects
+        for t in ts:
+            if t is not None and t.get_device() != index:
+                break
+        else:
+            return
     ts = [t for t in ts if t is not None]
     dev = ts[0].device
     for t in ts[1:]:
@@ -541,7 +553,7 @@ def int4_mm(x: torch.Tensor, B: torch.Tensor, b_scales: torch.Tensor, b_zeros: t
     if bias is not None:
         _need(bias, "bias", (torch.bfloat16,), 1, (N,))
     if C is None:
-        C = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
+        C = x.new_empty((M, N))
     else:
         _need(C, "C", (torch.bfloat16,), 2, (M, N))
     _one_device(x, B, b_scales, b_zeros, bias, C)
@@ -562,7 +574,7 @@ def grouped_int4_mm(x: torch.Tensor, B: torch.Tensor, b_scales: torch.Tensor, ex
     T, N, K, group = _int4_operands(x, B, b_scales, b_zeros, (E,))
     _need(expert_offsets, "expert_offsets", (torch.int32,), 1, (E + 1,))
     if C is None:
-        C = torch.empty((T, N), dtype=torch.bfloat16, device=x.device)
+        C = x.new_empty((T, N))
     else:
         _need(C, "C", (torch.bfloat16,), 2, (T, N))
     _one_device(x, B, b_scales, b_zeros, expert_offsets, C)
@@ -577,17 +589,20 @@ def moe_sort(topk_ids: torch.Tensor, num_experts: int, expert_offsets=None, orde
     [0, num_experts) take no row (slot -1)."""
     _need(topk_ids, "topk_ids", (torch.int32, torch.int64), 2)
     T, k = topk_ids.shape
-    E = int(num_experts)
+    E, n = int(num_experts), T * k
+    if expert_offsets is None and order is None and slots is None:   # one allocation, three views
+        expert_offsets, order, slots = topk_ids.new_empty(E + 1 + 2 * n, dtype=torch.int32).split((E + 1, n, n))
+        slots = slots.view(T, k)
     outs = []
-    for name, t, shape in (("expert_offsets", expert_offsets, (E + 1,)), ("order", order, (T * k,)),
+    for name, t, shape in (("expert_offsets", expert_offsets, (E + 1,)), ("order", order, (n,)),
                            ("slots", slots, (T, k))):
         if t is None:
-            t = torch.empty(shape, dtype=torch.int32, device=topk_ids.device)
+            t = topk_ids.new_empty(shape, dtype=torch.int32)
         else:
             _need(t, name, (torch.int32,), len(shape), shape)
         outs.append(t)
     _one_device(topk_ids, *outs)
-    _check("lq_moe_sort", lib().lq_moe_sort(_ptr(topk_ids), topk_ids.element_size(), T * k, E, *map(_ptr, outs),
+    _check("lq_moe_sort", lib().lq_moe_sort(_ptr(topk_ids), topk_ids.element_size(), n, E, *map(_ptr, outs),
                                             _stream(stream)))
     return tuple(outs)
 
@@ -607,7 +622,7 @@ def moe_permute(x: torch.Tensor, slots: torch.Tensor, xs: torch.Tensor | None = 
     T, H = x.shape
     k = _token_slots(slots, T)
     if xs is None:
-        xs = torch.empty((T * k, H), dtype=torch.bfloat16, device=x.device)
+        xs = x.new_empty((T * k, H))
     else:
         _need(xs, "xs", (torch.bfloat16,), 2, (xs.shape[0], H))
     _one_device(x, slots, xs)
@@ -647,7 +662,7 @@ def moe_unpermute(y: torch.Tensor, slots: torch.Tensor, weights: torch.Tensor | 
     if weights is not None:
         _need(weights, "weights", (torch.float32,), 2, (T, k))
     if out is None:
-        out = torch.empty((T, H), dtype=torch.bfloat16, device=y.device)
+        out = y.new_empty((T, H))
     else:
         _need(out, "out", (torch.bfloat16,), 2, (T, H))
     _one_device(y, slots, weights, out)
@@ -675,11 +690,11 @@ def moe_unpermute_backward(dout: torch.Tensor, y: torch.Tensor, slots: torch.Ten
     _need(dout, "dout", (torch.bfloat16,), 2, (T, H))
     _need(weights, "weights", (torch.float32,), 2, (T, k))
     if dy is None:
-        dy = torch.empty((P, H), dtype=torch.bfloat16, device=y.device)
+        dy = y.new_empty((P, H))
     else:
         _need(dy, "dy", (torch.bfloat16,), 2, (P, H))
     if dweights is None:
-        dweights = torch.empty((T, k), dtype=torch.float32, device=y.device)
+        dweights = weights.new_empty((T, k))
     else:
         _need(dweights, "dweights", (torch.float32,), 2, (T, k))
     _one_device(dout, y, slots, weights, dy, dweights)

@@ -484,8 +484,8 @@ lq_status lq_quant_weight_int4(const void *w, int64_t group, void *q, void *scal
  *              (or NULL) as above.
  *   bias     : [N] bf16 or NULL, added in fp32 before the rounding.
  *   C        : [M, N] bf16 out, 16-byte aligned.
- *   K        : a positive multiple of group; N % 8 == 0.  M == 0 or N == 0 is
- *              a no-op.
+ *   K        : a positive multiple of group, at most 2^24; N % 8 == 0.
+ *              M == 0 or N == 0 is a no-op.
  * The codes minus the zero points are exact in bf16, a group's products are
  * summed in fp32 and then multiplied by the group's scale in fp32.
  * Errors: LQ_ERR_INVALID_ARG, LQ_ERR_ALIGNMENT, LQ_ERR_UNSUPPORTED_SHAPE

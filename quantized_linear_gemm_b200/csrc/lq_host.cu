@@ -664,6 +664,34 @@ bool parse_table_file(const char* path, std::vector<TableEntry>* out, std::strin
 
 }  // namespace
 
+// What the other host file (lq_host_moe_int4.cu) and its launchers use of this one.
+namespace lq {
+
+bool encode_tma_2d(CUtensorMap* map, CUtensorMapDataType type, const void* ptr, int64_t inner, int64_t rows,
+                   int64_t row_bytes, int box_inner, int box_rows, CUtensorMapSwizzle swizzle) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[2] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(rows)};
+  cuuint64_t strides[1] = {static_cast<cuuint64_t>(row_bytes)};
+  cuuint32_t box[2] = {static_cast<cuuint32_t>(box_inner), static_cast<cuuint32_t>(box_rows)};
+  cuuint32_t estr[2] = {1u, 1u};
+  return fn(map, type, 2, const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+int device_status_word(cudaStream_t stream, int** status, uint64_t* limit_ns) {
+  DeviceState* d = nullptr;
+  const lq_status rc = device_state(stream, &d);
+  if (rc != LQ_OK) return rc;
+  *status = d->status;
+  *limit_ns = wait_limit_ns();
+  return LQ_OK;
+}
+
+bool static_weights_declared() { return g_static_weights.load() != 0; }
+
+}  // namespace lq
+
 // ======================================================================
 extern "C" {
 

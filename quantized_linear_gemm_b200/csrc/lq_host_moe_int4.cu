@@ -33,7 +33,7 @@ lq_status int4_mm_impl(const void* x, const void* B, const void* scales, const v
       (offsets && !aligned(offsets, 4)))
     return LQ_ERR_ALIGNMENT;
   if (K == 0 || K % group != 0 || N % 8 != 0) return LQ_ERR_UNSUPPORTED_SHAPE;
-  if (M > kMaxInt || K > kMaxInt || E > kMaxInt || N > kMaxInt || E * N > kMaxInt) return LQ_ERR_UNSUPPORTED_SHAPE;
+  if (M > kMaxInt || K > (int64_t(1) << 24) || E > kMaxInt || N > kMaxInt || E * N > kMaxInt) return LQ_ERR_UNSUPPORTED_SHAPE;
   lq::Int4Params p{};
   p.x = static_cast<const __nv_bfloat16*>(x);
   p.B = static_cast<const uint8_t*>(B);
@@ -46,8 +46,11 @@ lq_status int4_mm_impl(const void* x, const void* B, const void* scales, const v
   p.K = K;
   p.expert_offsets = grouped ? offsets : nullptr;
   p.num_experts = static_cast<int>(E);
-  const int64_t tiles = (M + 15) / 16 + (grouped ? (E < M ? E : M) : 0);   // token tiles, the grid's y
-  if (M > 8 && tiles > 65535) return LQ_ERR_UNSUPPORTED_SHAPE;
+  p.early_weights = lq::static_weights_declared() ? 1 : 0;
+  const int per_block = static_cast<int>(128 / group);   // groups per 128-wide block
+  p.vec_scales = K % 128 == 0 && aligned(scales, 2 * per_block) && (!zeros || aligned(zeros, per_block));
+  const int rc = lq::device_status_word(stream, &p.status, &p.wait_limit_ns);
+  if (rc != LQ_OK) return static_cast<lq_status>(rc);
   return launched(lq::launch_int4_mm(p, static_cast<int>(group), stream));
 }
 

@@ -120,7 +120,21 @@ struct Int4Params {
   int64_t M, N, K;
   const int* expert_offsets;   // grouped: device [num_experts + 1], N rows of B per expert; null = one product
   int num_experts;
+  int early_weights;           // stream weights before the grid dependency wait
+  int vec_scales;              // a block's scales (and zero points) may be loaded as one aligned word
+  int tile_tokens;             // tokens of a full tile, filled by the launcher
+  int* status;                 // device status word
+  uint64_t wait_limit_ns;
 };
+// Tiled 2-D tensor map of rows of `inner` elements, boxes of box_inner x
+// box_rows; out-of-range elements read as zero (lq_host.cu).
+bool encode_tma_2d(CUtensorMap* map, CUtensorMapDataType type, const void* ptr, int64_t inner, int64_t rows,
+                   int64_t row_bytes, int box_inner, int box_rows, CUtensorMapSwizzle swizzle);
+// Status word and wait limit of the current device, created on first use
+// (refused while `stream` is capturing), and the static-weights declaration
+// (lq_host.cu).  Returns an lq_status.
+int device_status_word(cudaStream_t stream, int** status, uint64_t* wait_limit_ns);
+bool static_weights_declared();
 cudaError_t launch_int4_mm(const Int4Params& p, int group, cudaStream_t stream);
 cudaError_t launch_quant_weight_int4(const void* w, int group, void* q, void* scales, void* zeros, int64_t N,
                                      int64_t K, cudaStream_t stream);

@@ -1,4 +1,5 @@
-// 4-bit weight codes -> bf16, shared by the 4-bit weight kernels.
+// 4-bit weight codes -> bf16, and the tiles of a grouped product, shared by the
+// 4-bit weight kernels.
 //
 // A 32-bit word holds the codes of 8 consecutive k, code i in bits
 // [4 i, 4 i + 4).  A bf16 whose exponent field is 0 or 1 is the plain integer
@@ -50,6 +51,51 @@ __device__ __forceinline__ void int4_word_to_bf16(uint32_t w, uint32_t offset, u
   out[1] = bf16x2_fma(byte_select(lo, hi, 0x8581), kInt4Factors, offset);
   out[2] = bf16x2_fma(byte_select(lo, hi, 0x8682), kInt4Factors, offset);
   out[3] = bf16x2_fma(byte_select(lo, hi, 0x8783), kInt4Factors, offset);
+}
+
+// The expert that owns token tile `tile` when every expert's rows are cut
+// into tiles of `per` tokens: its rows [*lo, *hi) of the tile.  Offsets are
+// clamped to [0, T] and to their running maximum, so a malformed table never
+// leads outside the rows.  Called by whole warps; false: no such tile.
+__device__ __forceinline__ bool find_expert_tile(const int* __restrict__ offsets, int E, int T, int per, int tile,
+                                                 int* expert, int* lo, int* hi) {
+  const int lane = threadIdx.x & 31;
+  int before = 0;                        // tiles of the experts so far
+  int carry = __ldg(offsets);            // running maximum so far
+  carry = carry < 0 ? 0 : (carry > T ? T : carry);
+  for (int e0 = 0; e0 < E; e0 += 32) {
+    const int e = e0 + lane;
+    int end = e < E ? __ldg(offsets + e + 1) : 0;
+    end = end < 0 ? 0 : (end > T ? T : end);
+    end = end > carry ? end : carry;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, end, o);
+      if (lane >= o && v > end) end = v;
+    }
+    int begin = __shfl_up_sync(0xffffffffu, end, 1);
+    if (lane == 0) begin = carry;
+    const int tiles = e < E ? (end - begin + per - 1) / per : 0;
+    int upto = tiles;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += v;
+    }
+    const int mine = before + upto - tiles;   // first tile of this lane's expert
+    const uint32_t has = __ballot_sync(0xffffffffu, tile >= mine && tile < mine + tiles);
+    if (has) {
+      const int src = __ffs(has) - 1;
+      const int b = __shfl_sync(0xffffffffu, begin, src), en = __shfl_sync(0xffffffffu, end, src);
+      *expert = e0 + src;
+      *lo = b + (tile - __shfl_sync(0xffffffffu, mine, src)) * per;
+      *hi = *lo + per < en ? *lo + per : en;
+      return true;
+    }
+    before += __shfl_sync(0xffffffffu, upto, 31);
+    carry = __shfl_sync(0xffffffffu, end, 31);
+  }
+  return false;
 }
 
 }  // namespace lq

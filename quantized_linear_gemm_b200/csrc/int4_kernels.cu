@@ -118,51 +118,6 @@ __device__ __forceinline__ void ldg_words(const uint8_t* p, uint32_t* out) {
     asm volatile("ld.global.nc.L2::256B.b32 %0, [%1];" : "=r"(out[0]) : "l"(p));
 }
 
-// The expert that owns token tile `tile` when every expert's rows are cut
-// into tiles of `per` tokens: its rows [*lo, *hi) of the tile.  Offsets are
-// clamped to [0, T] and to their running maximum, so a malformed table never
-// leads outside the rows.  Called by whole warps; false: no such tile.
-__device__ __forceinline__ bool find_expert_tile(const int* __restrict__ offsets, int E, int T, int per, int tile,
-                                                 int* expert, int* lo, int* hi) {
-  const int lane = threadIdx.x & 31;
-  int before = 0;                        // tiles of the experts so far
-  int carry = __ldg(offsets);            // running maximum so far
-  carry = carry < 0 ? 0 : (carry > T ? T : carry);
-  for (int e0 = 0; e0 < E; e0 += 32) {
-    const int e = e0 + lane;
-    int end = e < E ? __ldg(offsets + e + 1) : 0;
-    end = end < 0 ? 0 : (end > T ? T : end);
-    end = end > carry ? end : carry;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, end, o);
-      if (lane >= o && v > end) end = v;
-    }
-    int begin = __shfl_up_sync(0xffffffffu, end, 1);
-    if (lane == 0) begin = carry;
-    const int tiles = e < E ? (end - begin + per - 1) / per : 0;
-    int upto = tiles;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, upto, o);
-      if (lane >= o) upto += v;
-    }
-    const int mine = before + upto - tiles;   // first tile of this lane's expert
-    const uint32_t has = __ballot_sync(0xffffffffu, tile >= mine && tile < mine + tiles);
-    if (has) {
-      const int src = __ffs(has) - 1;
-      const int b = __shfl_sync(0xffffffffu, begin, src), en = __shfl_sync(0xffffffffu, end, src);
-      *expert = e0 + src;
-      *lo = b + (tile - __shfl_sync(0xffffffffu, mine, src)) * per;
-      *hi = *lo + per < en ? *lo + per : en;
-      return true;
-    }
-    before += __shfl_sync(0xffffffffu, upto, 31);
-    carry = __shfl_sync(0xffffffffu, end, 31);
-  }
-  return false;
-}
-
 template <int G, int MT, int RT, int W, bool kZeros>
 __global__ void __launch_bounds__(32 * W) int4_stream_kernel(const Int4Params p) {
   constexpr int kRows = 16 * RT, kTokens = 8 * MT;

@@ -688,6 +688,8 @@ int device_status_word(cudaStream_t stream, int** status, uint64_t* limit_ns) {
   return LQ_OK;
 }
 
+int skipped_block() { return g_skip_stage.load(); }
+
 bool static_weights_declared() { return g_static_weights.load() != 0; }
 
 }  // namespace lq

@@ -20,6 +20,31 @@ lq_status launched(cudaError_t e) {
 
 bool group_ok(int64_t group) { return group == 32 || group == 64 || group == 128; }
 
+// Which kernel a product takes: tile = 0, the streaming kernel (mma.sync, at
+// most 16 tokens per tile); else the tensor-core kernel with that many tokens
+// per tile and K shared by `split` CTAs.  `tokens`: of the product, or of one
+// expert on average.
+//
+// Measured on B200, G = 128, us (streaming / tensor core): 1 token
+// [4096, 4096] 4.7 / 6.5, [24576, 4096] 15.5 / 25.8, [4096, 12288] 9.9 / 11.5,
+// [5120, 25600] 32.8 / 24.9; 16 tokens 10.2 / 7.0, 27.3 / 25.9, 23.1 / 12.0,
+// 66.5 / 25.5.  The split fills up to 128 of the 148 SMs: a next launch that
+// is already resident (programmatic dependent launch) leaves one CTA per SM,
+// and clusters do not pack every GPC (48 tiles x 3 took 13.6 us, x 2 8.5).
+struct TensorPlan {
+  int tile, split;
+};
+
+TensorPlan tensor_plan(int64_t tokens, int64_t N, int64_t K, bool grouped) {
+  if (tokens <= 8 && (grouped || K <= 16384)) return {0, 1};
+  const int tile = tokens <= 16 ? 16 : tokens <= 32 ? 32 : tokens <= 64 ? 64 : tokens <= 128 ? 128 : 256;
+  if (grouped) return {tile, 1};
+  const int64_t tiles = ((N + 127) / 128) * ((tokens + tile - 1) / tile);
+  int split = 1;
+  while (split < 8 && tiles * (split + 1) <= 128 && (K + 127) / 128 >= 4 * (split + 1)) ++split;
+  return {tile, split};
+}
+
 // Shared by the dense (E = 1) and grouped products.
 lq_status int4_mm_impl(const void* x, const void* B, const void* scales, const void* zeros, const void* bias, void* C,
                        const int32_t* offsets, bool grouped, int64_t E, int64_t M, int64_t N, int64_t K,
@@ -51,6 +76,9 @@ lq_status int4_mm_impl(const void* x, const void* B, const void* scales, const v
   p.vec_scales = K % 128 == 0 && aligned(scales, 2 * per_block) && (!zeros || aligned(zeros, per_block));
   const int rc = lq::device_status_word(stream, &p.status, &p.wait_limit_ns);
   if (rc != LQ_OK) return static_cast<lq_status>(rc);
+  p.skip_block = lq::skipped_block();
+  const TensorPlan plan = tensor_plan(grouped ? (M + E - 1) / E : M, N, K, grouped);
+  if (plan.tile) return launched(lq::launch_int4_mma(p, static_cast<int>(group), plan.tile, plan.split, stream));
   return launched(lq::launch_int4_mm(p, static_cast<int>(group), stream));
 }
 

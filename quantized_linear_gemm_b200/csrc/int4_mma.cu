@@ -164,10 +164,10 @@ __global__ void __launch_bounds__(kMmaThreads, MmaShape<NT>::kTwo ? 2 : 1)
     const uint64_t desc0 = smem_desc_k_sw128(ring + kWeightTile);
     const bool leader = elect_one();
     int s = 0, b = 0;
-    uint32_t s_phase = 0, b_phase = 0;
+    uint32_t b_phase = 0;
     for (int i = 0; i < blocks; ++i) {
-      const bool ready = mbar_wait(&full[s], s_phase, p.wait_limit_ns) && mbar_wait(&a_full[b], b_phase, p.wait_limit_ns);
-      if (!__all_sync(0xffffffffu, ready)) {
+      // the converting warps waited for the block's copies, activations included, before they arrived here
+      if (!__all_sync(0xffffffffu, mbar_wait(&a_full[b], b_phase, p.wait_limit_ns))) {
         if (leader) give_up(10);
         break;
       }
@@ -182,10 +182,7 @@ __global__ void __launch_bounds__(kMmaThreads, MmaShape<NT>::kTwo ? 2 : 1)
         mma_commit(&empty[s]);
       }
       __syncwarp();
-      if (++s == kRing) {
-        s = 0;
-        s_phase ^= 1;
-      }
+      s = s + 1 == kRing ? 0 : s + 1;
       if (++b == kA) {
         b = 0;
         b_phase ^= 1;

@@ -295,7 +295,7 @@ int max_persistent_stages(int tile_n, int persistent = 1) {
 }
 
 // Streaming multiprocessors of the current device (148 on B200).
-int sm_count() {
+int device_sm_count() {
   static int cached[kMaxDevices] = {};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return kNumSms;
@@ -416,7 +416,7 @@ int pair_launch_smem(int fmt, int tile_n, int stages) {
 dim3 pair_grid(int fmt, int64_t M, int64_t gy, int split_k, int tile_n, bool bias, int smem_bytes) {
   const int64_t units = ((M + 255) / 256) * gy * split_k;
   int cap = pair_capacity(fmt, tile_n, bias, smem_bytes);
-  if (cap <= 0) cap = sm_count() / 2;
+  if (cap <= 0) cap = device_sm_count() / 2;
   const int64_t pairs = units < cap ? units : cap;
   return dim3(static_cast<unsigned>(2 * pairs), 1, 1);
 }
@@ -542,7 +542,7 @@ lq_status scaled_mm_impl(int fmt, const void* A, const float* a_s, const void* B
   p.bias = static_cast<const __nv_bfloat16*>(bias);
   if (v.persistent == 3) {   // stream-K: one partial slot [128 x tile_n] per CTA, and the ready flags
     const int64_t iters = ((M + 127) / 128) * gy * p.T;
-    const int64_t ctas = iters < sm_count() ? iters : sm_count();
+    const int64_t ctas = iters < device_sm_count() ? iters : device_sm_count();
     if (ctas > kMaxStreamKCtas) return LQ_ERR_UNSUPPORTED_SHAPE;
     rc = ensure_workspace(d, static_cast<size_t>(ctas) * 128u * static_cast<size_t>(v.tile_n) * 4u, stream);
     if (rc != LQ_OK) return rc;
@@ -575,14 +575,14 @@ lq_status scaled_mm_impl(int fmt, const void* A, const float* a_s, const void* B
                                    lq::tmem_cols_per_cta(fmt, v.tile_n, 0));
   if (v.persistent == 1) {   // one CTA per SM (at most one per tile), each looping over tiles
     const int64_t tiles = gx * gy;
-    const int64_t ctas = tiles < sm_count() ? tiles : sm_count();
+    const int64_t ctas = tiles < device_sm_count() ? tiles : device_sm_count();
     l.grid = dim3(static_cast<unsigned>(ctas), 1, 1);
     l.smem_bytes = tmem_bounded_smem(lq::persistent_smem_bytes_for(v.tile_n, v.stages),
                                      lq::tmem_cols_per_cta(fmt, v.tile_n, 1));
     l.persistent = 1;
   } else if (v.persistent == 3) {   // stream-K: one CTA per SM splitting tiles x K blocks
     const int64_t iters = ((M + 127) / 128) * gy * p.T;
-    const int64_t ctas = iters < sm_count() ? iters : sm_count();
+    const int64_t ctas = iters < device_sm_count() ? iters : device_sm_count();
     l.grid = dim3(static_cast<unsigned>(ctas), 1, 1);
     l.smem_bytes = tmem_bounded_smem(lq::persistent_smem_bytes_for(v.tile_n, v.stages),
                                      lq::tmem_cols_per_cta(fmt, v.tile_n, 3));
@@ -687,6 +687,8 @@ int device_status_word(cudaStream_t stream, int** status, uint64_t* limit_ns) {
   *limit_ns = wait_limit_ns();
   return LQ_OK;
 }
+
+int sm_count() { return device_sm_count(); }
 
 int skipped_block() { return g_skip_stage.load(); }
 
@@ -1097,7 +1099,7 @@ size_t lq_workspace_bytes(lq_fmt fmt, int64_t M, int64_t N, int64_t K, const lq_
   const lq_variant v = variant ? *variant : default_variant(static_cast<int>(fmt), M, N, K);
   if (v.persistent == 3 && !v.swap_ab && v.tile_n > 0) {   // stream-K partial slots
     const int64_t iters = ((M + 127) / 128) * ((N + v.tile_n - 1) / v.tile_n) * ((K + 127) / 128);
-    const int64_t ctas = iters < sm_count() ? iters : sm_count();
+    const int64_t ctas = iters < device_sm_count() ? iters : device_sm_count();
     return static_cast<size_t>(ctas) * 128u * static_cast<size_t>(v.tile_n) * 4u;
   }
   if (v.split_k <= 1 || v.reduce == 2) return 0;
@@ -1248,7 +1250,7 @@ extern "C" lq_status lq_scaled_mm_noalloc(lq_fmt fmt_, const void* A, const floa
                                    lq::tmem_cols_per_cta(fmt, v.tile_n, 0));
   if (v.persistent == 1) {   // split_k 1: no scratch; one CTA per SM looping over tiles
     const int64_t tiles = gx * gy;
-    const int64_t ctas = tiles < sm_count() ? tiles : sm_count();
+    const int64_t ctas = tiles < device_sm_count() ? tiles : device_sm_count();
     l.grid = dim3(static_cast<unsigned>(ctas), 1, 1);
     l.smem_bytes = tmem_bounded_smem(lq::persistent_smem_bytes_for(v.tile_n, v.stages),
                                      lq::tmem_cols_per_cta(fmt, v.tile_n, 1));

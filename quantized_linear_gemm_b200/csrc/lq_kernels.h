@@ -122,6 +122,7 @@ struct Int4Params {
   int num_experts;
   int early_weights;           // stream weights before the grid dependency wait
   int vec_scales;              // a block's scales (and zero points) may be loaded as one aligned word
+  int split;                   // CTAs (a cluster) that share a tile's K (tensor-core kernel)
   int skip_block;              // test hook: >= 0 = the 128-wide K block that is never loaded (tensor-core kernel)
   int* status;                 // device status word
   uint64_t wait_limit_ns;
@@ -134,6 +135,8 @@ bool encode_tma_2d(CUtensorMap* map, CUtensorMapDataType type, const void* ptr, 
 // (refused while `stream` is capturing), and the static-weights declaration
 // (lq_host.cu).  Returns an lq_status.
 int device_status_word(cudaStream_t stream, int** status, uint64_t* wait_limit_ns);
+int sm_count();        // streaming multiprocessors of the current device
+int int4_mma_max_experts();
 int skipped_block();   // lq_test_inject_stall's K tile, -1 when off
 bool static_weights_declared();
 // The tensor-core kernel: `tile` tokens per tile (16, 32, 64, 128 or 256), K shared by `split` CTAs (a cluster, 1..8).

@@ -591,16 +591,18 @@ def moe_sort(topk_ids: torch.Tensor, num_experts: int, expert_offsets=None, orde
     T, k = topk_ids.shape
     E, n = int(num_experts), T * k
     if expert_offsets is None and order is None and slots is None:   # one allocation, three views
-        expert_offsets, order, slots = topk_ids.new_empty(E + 1 + 2 * n, dtype=torch.int32).split((E + 1, n, n))
-        slots = slots.view(T, k)
-    outs = []
-    for name, t, shape in (("expert_offsets", expert_offsets, (E + 1,)), ("order", order, (n,)),
-                           ("slots", slots, (T, k))):
-        if t is None:
-            t = topk_ids.new_empty(shape, dtype=torch.int32)
-        else:
-            _need(t, name, (torch.int32,), len(shape), shape)
-        outs.append(t)
+        buf = topk_ids.new_empty(max(E, 0) + 1 + 2 * n, dtype=torch.int32)
+        outs = [buf.as_strided((max(E, 0) + 1,), (1,), 0), buf.as_strided((n,), (1,), max(E, 0) + 1),
+                buf.as_strided((T, k), (k, 1), max(E, 0) + 1 + n)]
+    else:
+        outs = []
+        for name, t, shape in (("expert_offsets", expert_offsets, (E + 1,)), ("order", order, (n,)),
+                               ("slots", slots, (T, k))):
+            if t is None:
+                t = topk_ids.new_empty(shape, dtype=torch.int32)
+            else:
+                _need(t, name, (torch.int32,), len(shape), shape)
+            outs.append(t)
     _one_device(topk_ids, *outs)
     _check("lq_moe_sort", lib().lq_moe_sort(_ptr(topk_ids), topk_ids.element_size(), n, E, *map(_ptr, outs),
                                             _stream(stream)))

@@ -486,10 +486,17 @@ lq_status lq_quant_weight_int4(const void *w, int64_t group, void *q, void *scal
  *   C        : [M, N] bf16 out, 16-byte aligned.
  *   K        : a positive multiple of group, at most 2^24; N % 8 == 0.
  *              M == 0 or N == 0 is a no-op.
- * The codes minus the zero points are exact in bf16, a group's products are
- * summed in fp32 and then multiplied by the group's scale in fp32.
+ * Up to 8 tokens (16 rows of a grouped call) the codes minus the zero points
+ * are exact, a group's products are summed in fp32 and then multiplied by the
+ * group's scale in fp32; for more tokens, and for few tokens of long or
+ * finely grouped rows, the weight (q - z) s is rounded once to bf16 and
+ * multiplied on the tensor core with fp32 sums.  |b_scales| < 2^34; sums below
+ * 2^-60 in magnitude may lose precision.  No workspace: calls on different
+ * streams may overlap.  Reads B only after the previous kernels on the stream
+ * have finished unless lq_declare_static_weights(1) was called.
  * Errors: LQ_ERR_INVALID_ARG, LQ_ERR_ALIGNMENT, LQ_ERR_UNSUPPORTED_SHAPE
- * before any launch; LQ_ERR_CUDA.
+ * before any launch; LQ_ERR_WORKSPACE when the device has not been initialised
+ * and the stream is capturing; LQ_ERR_CUDA.
  */
 lq_status lq_int4_mm(const void *x, const void *B, const void *b_scales,
                      const void *b_zeros, const void *bias, void *C, int64_t M,
@@ -499,7 +506,8 @@ lq_status lq_int4_mm(const void *x, const void *B, const void *b_scales,
  * Grouped (mixture-of-experts) product with 4-bit weights: x [T, K] sorted by
  * expert, B [E, N, K / 2], b_scales and b_zeros [E, N, K / group], C [T, N].
  * expert_offsets as for lq_grouped_scaled_mm (clamped to [0, T] and to their
- * running maximum); rows of C outside every expert are left as they were.
+ * running maximum; the last may be below T); rows of C outside every expert are
+ * left as they were, and rows of x outside every expert do not matter.
  * E * N < 2^31.  Errors as lq_int4_mm; LQ_ERR_INVALID_ARG for E = 0 with T > 0.
  */
 lq_status lq_grouped_int4_mm(const void *x, const void *B, const void *b_scales,
@@ -650,8 +658,8 @@ lq_status lq_set_trace(uint64_t *device_buffer);
 
 /*
  * Test hook for failure detection.  While k_tile >= 0, every scaled_mm
- * kernel launched afterwards leaves the k_tile-th K tile of each CTA
- * unloaded, so the tensor-core warp's bounded wait for it runs out: the
+ * kernel launched afterwards leaves the k_tile-th K tile of each CTA (every
+ * tensor-core 4-bit product: the k_tile-th 128-wide block of K) unloaded, so the tensor-core warp's bounded wait for it runs out: the
  * kernel sets the device status word, drains its copies, frees its tensor
  * memory and returns (C undefined), and lq_device_status reports
  * LQ_ERR_DEVICE_TIMEOUT.  Nothing faults or hangs.  wait_limit_ns > 0

@@ -30,7 +30,7 @@ bool group_ok(int64_t group) { return group == 32 || group == 64 || group == 128
 // 66.5 / 22.  G = 64, [24576, 4096], 8 tokens 25 / 20.5 (the streaming kernel
 // loads 8 bytes at a time there).  The split fills the CTAs that fit at once
 // (two per SM up to 64 tokens, one beyond; clusters do not pack every GPC, so
-// 256 and 128 of them) as long as each keeps at least 8 blocks: [5120, 25600]
+// 240 and 128 of them; 256 fit on some GPUs only) as long as each keeps at least 8 blocks: [5120, 25600]
 // at 64 tokens 101 us whole, 28 us in 6 parts, 45 us in 7 (280 CTAs).
 // Grouped, 128 experts, [1536, 2048] each: 8 rows 7.1 / 10.6, 64 rows 35 / 29,
 // 512 rows 86 / 56.  Its tile covers one and a half times the average expert:
@@ -48,7 +48,7 @@ TensorPlan tensor_plan(int64_t M, int64_t N, int64_t K, int64_t group, int64_t e
   }
   if (M <= 8 && K <= 16384 && (group != 64 || N < 16384)) return {0, 1};
   const int tile = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : M <= 128 ? 128 : 256;
-  const int64_t tiles = ((N + 127) / 128) * ((M + tile - 1) / tile), room = tile <= 64 ? 256 : 128;
+  const int64_t tiles = ((N + 127) / 128) * ((M + tile - 1) / tile), room = tile <= 64 ? 240 : 128;
   int split = 1;
   while (split < 8 && tiles * (split + 1) <= room && (K + 127) / 128 >= 8 * (split + 1)) ++split;
   return {tile, split};

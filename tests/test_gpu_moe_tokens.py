@@ -294,3 +294,89 @@ def test_int4_expert_layer(cuda_device):
     # y is off by at most H 2^-23 S and half a bf16 step; the combination adds its own k terms and one rounding
     e = (H * 2.0 ** -23 + 2.0 ** -8 * (1 + H * 2.0 ** -23) + k * 2.0 ** -22) * mag
     assert np.all(np.abs(bf16_to_f64(out) - r) <= e + 2.0 ** -8 * (np.abs(r) + e))
+
+
+def test_rows_past_2_31_elements(cuda_device):
+    """Slots whose rows lie past 2^31 elements: dispatch, combination and the gradients against torch indexing."""
+    tokens, k, H = 140000, 8, 2048
+    n = tokens * k
+    assert n * H > 2 ** 31
+    g = torch.Generator(device="cuda").manual_seed(1)
+    ids = torch.rand((tokens, 16), generator=g, device="cuda").topk(k, 1).indices
+    off, order, slots = lq.moe_sort(ids, 16)
+    assert int(off[-1]) == n
+    flat = ids.reshape(-1)
+    assert torch.equal(order.long(), torch.argsort(flat, stable=True))
+    x = torch.randn((tokens, H), generator=g, device="cuda").bfloat16()
+    xs = lq.moe_permute(x, slots)
+    pick = torch.randint(0, n, (4000,), generator=g, device="cuda")
+    pick[0], pick[1] = n - 1, 0
+    assert torch.equal(xs[pick], x[order[pick].long() // k])
+    w = torch.full((tokens, k), 0.125, device="cuda")
+    assert torch.equal(lq.moe_unpermute(xs, slots, w), x)        # eight equal rows of weight 1/8: exact
+    dy, dw = lq.moe_unpermute_backward(x, xs, slots, w)
+    assert torch.equal(dy[pick], (x[order[pick].long() // k].float() * 0.125).bfloat16())
+    t = torch.randint(0, tokens, (50,), generator=g, device="cuda")
+    ref = (x[t].double() ** 2).sum(1)[:, None].expand(-1, k)
+    assert torch.all((dw[t].double() - ref).abs() <= H * 2.0 ** -23 * ref)
+
+
+def test_tokens_without_slots(cuda_device):
+    """k = 0: nothing to sum; no tokens: nothing to do."""
+    y = torch.randn((4, 64), device="cuda").bfloat16()
+    out = lq.moe_unpermute(y, torch.empty((3, 0), dtype=torch.int32, device="cuda"))
+    assert out.shape == (3, 64) and torch.all(out == 0)
+    assert lq.moe_permute(torch.empty((0, 64), dtype=torch.bfloat16, device="cuda"),
+                          torch.empty((0, 2), dtype=torch.int32, device="cuda")).shape == (0, 64)
+
+
+def test_slots_outside_the_rows_are_skipped(cuda_device):
+    """Slots past the last row or negative: neither read nor written (a short buffer, a foreign table)."""
+    tokens, k, H, P = 6, 3, 128, 10
+    g = np.random.default_rng(3)
+    slots = g.permutation(np.arange(-4, 14))[: tokens * k].reshape(tokens, k).astype(np.int32)
+    slots[0] = [2 ** 31 - 1, -2 ** 31, 10]
+    x = inputs.activations(tokens, H, seed=1)
+    y = inputs.activations(P, H, seed=2)
+    w = torch.rand((tokens, k), generator=torch.Generator().manual_seed(3))
+    base = torch.full((P + 2, H), 3.0, dtype=torch.bfloat16, device="cuda")
+    buf = base.clone()
+    lq.moe_permute(x.cuda(), cuda(slots), xs=buf[:P])
+    assert np.array_equal(buf[:P].float().cpu().numpy(), T.permute(x.float().numpy(), slots, np.full((P, H), 3.0)))
+    assert torch.all(buf[P:] == 3.0)
+    out = lq.moe_unpermute(y.cuda(), cuda(slots), w.cuda())
+    r, mag = T.unpermute(y.float().numpy(), slots, w.numpy())
+    e = k * 2.0 ** -23 * mag
+    assert np.all(np.abs(bf16_to_f64(out) - r) <= e + 2.0 ** -8 * (np.abs(r) + e))
+    buf = base.clone()
+    dy, dw = lq.moe_unpermute_backward(x.cuda(), y.cuda(), cuda(slots), w.cuda(), dy=buf[:P])
+    rdy, rdw, mag = T.unpermute_backward(x.float().numpy(), y.float().numpy(), slots, w.numpy(), np.full((P, H), 3.0))
+    assert np.all(np.abs(bf16_to_f64(dy) - rdy) <= np.abs(rdy) * (2.0 ** -8 + 2.0 ** -23))
+    assert np.all(np.abs(dw.cpu().numpy() - rdw) <= H * 2.0 ** -23 * mag) and torch.all(buf[P:] == 3.0)
+
+
+@pytest.mark.parametrize("op", ["sort", "permute", "unpermute", "backward"])
+def test_inputs_written_just_before(cuda_device, op):
+    """Each call reads what the kernel before it on the stream wrote (the launches overlap in part)."""
+    tokens, k, E, H = 64, 4, 8, 512
+    ids = [cuda(routing(tokens, k, E, seed=s)) for s in (1, 2)]
+    slots = [lq.moe_sort(i, E)[2] for i in ids]
+    x = [inputs.activations(tokens, H, seed=s).cuda() for s in (1, 2)]
+    y = [inputs.activations(tokens * k, H, seed=s).cuda() for s in (3, 4)]
+    w = torch.rand((tokens, k), device="cuda")
+    run = {"sort": lambda i, sl, x, y: lq.moe_sort(i, E), "permute": lambda i, sl, x, y: (lq.moe_permute(x, sl),),
+           "unpermute": lambda i, sl, x, y: (lq.moe_unpermute(y, sl, w),),
+           "backward": lambda i, sl, x, y: lq.moe_unpermute_backward(x, y, sl, w)}[op]
+    torch.cuda.synchronize()
+    want = []
+    for i in (0, 1):
+        want.append([t.clone() for t in run(ids[i], slots[i], x[i], y[i])])
+        torch.cuda.synchronize()
+    bufs = [torch.empty_like(t[0]) for t in (ids, slots, x, y)]
+    for n in range(20):
+        i = n & 1
+        for b, t in zip(bufs, (ids, slots, x, y)):
+            b.copy_(t[i])
+        got = run(*bufs)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want[i]))

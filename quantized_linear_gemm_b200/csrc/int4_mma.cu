@@ -34,7 +34,6 @@
 namespace lq {
 namespace {
 
-constexpr int kConvWarps = 8;           // two groups of four; group g converts every second block
 constexpr int kMaxRing = 8, kMaxA = 4;
 constexpr int kWeightTile = 128 * 64;   // bytes of a 128-row, 128-wide block of codes
 constexpr int kMaxGroupedExperts = 1024;
@@ -55,6 +54,10 @@ struct MmaShape {
   static constexpr int kD = NT == 128 ? 2 : 1;                   // accumulators
   static constexpr int kCols = kTwo ? 256 : 512;                 // tensor-memory columns
   static constexpr int kSmem = kRing * kStage + 1024;
+  // converting groups of four warps, group g takes blocks g, g + kGroups, ...; one keeps up with the
+  // MMAs of 256 tokens, and with 14 warps the epilogue has the registers for its packed columns
+  static constexpr int kGroups = NT == 256 ? 1 : 2;
+  static constexpr int kConvWarps = 4 * kGroups;
   static constexpr int kWarps = 2 + kConvWarps + (kTwo ? 0 : 8);
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kEpiFirst = kTwo ? 2 : 2 + kConvWarps;    // first of the eight epilogue warps
@@ -83,7 +86,7 @@ __global__ void __launch_bounds__(MmaShape<NT>::kThreads, MmaShape<NT>::kTwo ? 2
     int4_mma_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                     const Int4Params p) {
   using Sh = MmaShape<NT>;
-  constexpr int kRing = Sh::kRing, kA = Sh::kA, kD = Sh::kD;
+  constexpr int kRing = Sh::kRing, kA = Sh::kA, kD = Sh::kD, kGroups = Sh::kGroups;
   extern __shared__ uint8_t mma_smem_raw[];
   uint8_t* ring = mma_smem_raw + ((1024u - (smem_addr(mma_smem_raw) & 1023u)) & 1023u);
   __shared__ uint64_t full[kMaxRing], empty[kMaxRing], a_full[kMaxA], a_empty[kMaxA], d_full[2], d_empty[2];
@@ -303,7 +306,7 @@ __global__ void __launch_bounds__(MmaShape<NT>::kThreads, MmaShape<NT>::kTwo ? 2
     tc_fence_after_sync();
     const Tile t = tile_at(k);
     const int toks = t.m1 - t.m0;
-    constexpr int kCols = NT / 2, kChunk = NT == 256 ? 16 : (kCols % 32 == 0 ? 32 : (kCols % 16 == 0 ? 16 : 8));   // 256: registers
+    constexpr int kCols = NT / 2, kChunk = kCols % 32 == 0 ? 32 : (kCols % 16 == 0 ? 16 : 8);
     const int c0 = part * kCols;
     const uint32_t at = tm_d + d * NT + c0 + (static_cast<uint32_t>(quad * 32) << 16);
     const int64_t n = static_cast<int64_t>(t.n_tile) * 128 + quad * 32 + lane;
@@ -351,12 +354,12 @@ __global__ void __launch_bounds__(MmaShape<NT>::kThreads, MmaShape<NT>::kTwo ? 2
     }
   };
 
-  if (warp >= 2 && warp < 2 + kConvWarps) {
-    const int half = (warp - 2) >> 2;      // group
+  if (warp >= 2 && warp < 2 + Sh::kConvWarps) {
+    const int group_id = (warp - 2) >> 2;      // group
     const int row = quad * 32 + lane;
     constexpr int GB = 128 / G;            // groups in a block
     // cursor of the scales, one block (of this group) ahead of the conversion
-    int sc_tile = 0, sc_block = half;
+    int sc_tile = 0, sc_block = group_id;
     const __nv_bfloat16* sr = nullptr;
     const uint8_t* zr = nullptr;
     auto enter_tile = [&] {
@@ -379,7 +382,7 @@ __global__ void __launch_bounds__(MmaShape<NT>::kThreads, MmaShape<NT>::kTwo ? 2
       }
     };
     auto next_scales = [&] {               // this group's next block
-      sc_block += 2;
+      sc_block += kGroups;
       if (sc_block >= blocks) {
         do {
           sc_block -= blocks;
@@ -397,14 +400,14 @@ __global__ void __launch_bounds__(MmaShape<NT>::kThreads, MmaShape<NT>::kTwo ? 2
       if (sc_tile < mine) enter_tile();
       load_scales();
     }
-    int s = half % kRing, b = half;        // ring slot and converted-block slot
+    int s = group_id % kRing, b = group_id;        // ring slot and converted-block slot
     uint32_t s_phase = 0, b_phase = 1;     // the first kA blocks find their slot free
     const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
     const uint32_t swizzle = (row >> 1) & 3;
-    int k = 0, i = half, d = 0;            // tile, block
+    int k = 0, i = group_id, d = 0;            // tile, block
     uint32_t d_phase = 0;
     for (; k < mine && ok; ++k) {
-      for (; i < blocks; i += 2) {
+      for (; i < blocks; i += kGroups) {
         uint32_t factor[GB], offset[GB];
 #pragma unroll
         for (int j = 0; j < GB; ++j) {
@@ -457,18 +460,18 @@ __global__ void __launch_bounds__(MmaShape<NT>::kThreads, MmaShape<NT>::kTwo ? 2
         tc_fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(&a_full[b]);
-        s += 2;
+        s += kGroups;
         if (s >= kRing) {
           s -= kRing;
           s_phase ^= 1;
         }
-        b += 2;
+        b += kGroups;
         if (b >= kA) {
           b -= kA;
           b_phase ^= 1;
         }
       }
-      i -= blocks;                         // 0 or 1: the first block of the next tile that is this group's
+      i -= blocks;                         // the first block of the next tile that is this group's
       if constexpr (Sh::kTwo) {
         if (ok) epilogue(k, d, d_phase);
         if (++d == kD) {
@@ -534,6 +537,34 @@ __global__ void __launch_bounds__(MmaShape<NT>::kThreads, MmaShape<NT>::kTwo ? 2
   }
 }
 
+constexpr int kMaxSplit = 8;
+
+// Clusters of `split` CTAs that fit on the current device at once with one CTA
+// per SM (what the runtime's query counts for these kernels also where two run
+// side by side): 148 CTAs less what does not pack into a GPC, which differs
+// from GPU to GPU.  Cached; 0 if the query fails.
+int cluster_room(const void* kernel, cudaLaunchConfig_t cfg, int dev, std::atomic<int> (&cache)[64][kMaxSplit + 1],
+                 int split) {
+  std::atomic<int>& slot = cache[dev & 63][split];
+  int n = slot.load();
+  if (n == 0) {
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = static_cast<unsigned>(split);
+    attr.val.clusterDim.y = 1;
+    attr.val.clusterDim.z = 1;
+    cfg.gridDim = dim3(static_cast<unsigned>(split));
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
+      cudaGetLastError();
+      n = 0;
+    }
+    slot.store(n > 0 ? n : -1);
+  }
+  return n > 0 ? n : 0;
+}
+
 template <int G, int NT>
 cudaError_t launch_mma_gn(const Int4Params& params, cudaStream_t stream) {
   using Sh = MmaShape<NT>;
@@ -543,8 +574,6 @@ cudaError_t launch_mma_gn(const Int4Params& params, cudaStream_t stream) {
   if (p.expert_offsets) token_tiles += p.num_experts < p.M ? p.num_experts : p.M;   // a bound
   const int64_t tiles = ntiles * token_tiles;
   if (tiles > 0x7FFFFFFF / 2) return cudaErrorInvalidValue;   // the host checks this first
-  int64_t ctas = sm_count() * (Sh::kTwo ? 2 : 1);
-  if (p.split > 1 || ctas > tiles) ctas = tiles;
   CUtensorMap tmW, tmX;
   const int64_t rows = p.N * (p.expert_offsets ? p.num_experts : 1);
   if (!encode_tma_2d(&tmW, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.B, p.K / 2, rows, p.K / 2, 64, 128,
@@ -552,25 +581,49 @@ cudaError_t launch_mma_gn(const Int4Params& params, cudaStream_t stream) {
       !encode_tma_2d(&tmX, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p.x, p.K, p.M, p.K * 2, 64, NT,
                      CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;
-  auto kernel = p.zeros ? int4_mma_kernel<G, NT, true> : int4_mma_kernel<G, NT, false>;
+  const bool zeros = p.zeros != nullptr;
+  auto kernel = zeros ? int4_mma_kernel<G, NT, true> : int4_mma_kernel<G, NT, false>;
   static std::atomic<uint64_t> prepared[2];   // devices (by bit) whose kernel has its attributes, per kZeros
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   const uint64_t bit = uint64_t(1) << (dev & 63);
-  if (!(prepared[p.zeros != nullptr].load() & bit)) {
+  if (!(prepared[zeros].load() & bit)) {
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kSmem);
     // without it the driver may size the shared memory for one CTA per SM
     if (e == cudaSuccess)
       e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
     if (e != cudaSuccess) return e;
-    prepared[p.zeros != nullptr].fetch_or(bit);
+    prepared[zeros].fetch_or(bit);
   }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(ctas * p.split));
   cfg.blockDim = dim3(Sh::kThreads);
   cfg.dynamicSmemBytes = Sh::kSmem;
   cfg.stream = stream;
+
+  // Split-K: few tiles, each shared by a cluster of as many CTAs as find an SM
+  // of their own and keep at least 8 blocks each; two per SM only where that
+  // leaves them 48 blocks or more.  Measured on B200, us with splits 1..8:
+  // [4096, 4096], 16 tokens: 13.0 9.2 7.9 7.3 | 8.8 8.8 8.6 8.4 (two per SM from 5);
+  // [4096, 12288], 64 tokens: 42.2 25.2 19.8 16.8 | 20.3 18.8 18.8 18.6;
+  // [5120, 25600], 64 tokens: 86.9 47.9 34.6 | 35.7 31.4 28.3 44.5 40.6 (7 and 8 do not fit).
+  p.split = 1;
+  static std::atomic<int> room[2][64][kMaxSplit + 1];
+  if (!p.expert_offsets && tiles <= 148) {
+    const int64_t blocks = (p.K + 127) / 128;
+    auto widest = [&](int per_sm) {
+      for (int c = kMaxSplit; c > 1; --c)
+        if (blocks >= 8 * c &&
+            tiles <= per_sm * cluster_room(reinterpret_cast<const void*>(kernel), cfg, dev, room[zeros], c))
+          return c;
+      return 1;
+    };
+    p.split = widest(1);
+    if (Sh::kTwo && blocks >= 48 * p.split) p.split = widest(2);
+  }
+  int64_t ctas = sm_count() * (Sh::kTwo ? 2 : 1);
+  if (p.split > 1 || ctas > tiles) ctas = tiles;
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas * p.split));
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -598,9 +651,7 @@ cudaError_t launch_mma_g(const Int4Params& p, int tile, cudaStream_t stream) {
 
 int int4_mma_max_experts() { return kMaxGroupedExperts; }
 
-cudaError_t launch_int4_mma(const Int4Params& params, int group, int tile, int split, cudaStream_t stream) {
-  Int4Params p = params;
-  p.split = split;
+cudaError_t launch_int4_mma(const Int4Params& p, int group, int tile, cudaStream_t stream) {
   switch (group) {
     case 32: return launch_mma_g<32>(p, tile, stream);
     case 64: return launch_mma_g<64>(p, tile, stream);

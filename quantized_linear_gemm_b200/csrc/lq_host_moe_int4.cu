@@ -20,38 +20,26 @@ lq_status launched(cudaError_t e) {
 
 bool group_ok(int64_t group) { return group == 32 || group == 64 || group == 128; }
 
-// Which kernel a product takes: tile = 0, the streaming kernel (mma.sync, at
-// most 16 tokens per tile); else the tensor-core kernel with that many tokens
-// per tile and K shared by `split` CTAs.
+// Which kernel a product takes: 0, the streaming kernel (mma.sync, at most 16
+// tokens per tile); else the tensor-core kernel with that many tokens per tile.
 //
 // Measured on B200, us (streaming / tensor core).  Dense, G = 128: 1 token
 // [4096, 4096] 4.7 / 7.3, [24576, 4096] 15.5 / 19, [4096, 12288] 9.9 / 12.4,
-// [5120, 25600] 32.8 / 21.5; 16 tokens 10.2 / 7.3, 27.3 / 22, 23.1 / 12.4,
+// [5120, 25600] 32.8 / 21.5; 16 tokens 10.2 / 7.0, 27.3 / 22, 23.1 / 12.4,
 // 66.5 / 22.  G = 64, [24576, 4096], 8 tokens 25 / 20.5 (the streaming kernel
-// loads 8 bytes at a time there).  The split fills the CTAs that fit at once
-// (two per SM up to 64 tokens, one beyond; clusters do not pack every GPC, so
-// 240 and 128 of them; 256 fit on some GPUs only) as long as each keeps at least 8 blocks: [5120, 25600]
-// at 64 tokens 101 us whole, 28 us in 6 parts, 45 us in 7 (280 CTAs).
+// loads 8 bytes at a time there).
 // Grouped, 128 experts, [1536, 2048] each: 8 rows 7.1 / 10.6, 64 rows 35 / 29,
 // 512 rows 86 / 56.  Its tile covers one and a half times the average expert:
 // 2048 rows 75, 59, 64 us with tiles of 16, 32, 64; 32768 rows [2048, 768]
 // 204, 156, 175 us with 64, 128, 256.
-struct TensorPlan {
-  int tile, split;
-};
-
-TensorPlan tensor_plan(int64_t M, int64_t N, int64_t K, int64_t group, int64_t experts) {
+int tensor_tile(int64_t M, int64_t N, int64_t K, int64_t group, int64_t experts) {
   if (experts) {
-    if (M <= (experts > 1 ? 16 : 8) || experts > lq::int4_mma_max_experts()) return {0, 1};
+    if (M <= (experts > 1 ? 16 : 8) || experts > lq::int4_mma_max_experts()) return 0;
     const int64_t want = (M + M / 2) / experts;
-    return {want <= 16 ? 16 : want <= 32 ? 32 : want <= 64 ? 64 : want <= 1024 ? 128 : 256, 1};
+    return want <= 16 ? 16 : want <= 32 ? 32 : want <= 64 ? 64 : want <= 1024 ? 128 : 256;
   }
-  if (M <= 8 && K <= 16384 && (group != 64 || N < 16384)) return {0, 1};
-  const int tile = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : M <= 128 ? 128 : 256;
-  const int64_t tiles = ((N + 127) / 128) * ((M + tile - 1) / tile), room = tile <= 64 ? 240 : 128;
-  int split = 1;
-  while (split < 8 && tiles * (split + 1) <= room && (K + 127) / 128 >= 8 * (split + 1)) ++split;
-  return {tile, split};
+  if (M <= 8 && K <= 16384 && (group != 64 || N < 16384)) return 0;
+  return M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : M <= 128 ? 128 : 256;
 }
 
 // Shared by the dense (E = 1) and grouped products.
@@ -86,11 +74,11 @@ lq_status int4_mm_impl(const void* x, const void* B, const void* scales, const v
   const int rc = lq::device_status_word(stream, &p.status, &p.wait_limit_ns);
   if (rc != LQ_OK) return static_cast<lq_status>(rc);
   p.skip_block = lq::skipped_block();
-  const TensorPlan plan = tensor_plan(M, N, K, group, grouped ? E : 0);
+  const int tile = tensor_tile(M, N, K, group, grouped ? E : 0);
   const int64_t spare = grouped ? (E < M ? E : M) : 0;       // token tiles beyond M / tile, at most
-  if (plan.tile) {
-    if (((N + 127) / 128) * ((M + plan.tile - 1) / plan.tile + spare) > kMaxInt / 2) return LQ_ERR_UNSUPPORTED_SHAPE;
-    return launched(lq::launch_int4_mma(p, static_cast<int>(group), plan.tile, plan.split, stream));
+  if (tile) {
+    if (((N + 127) / 128) * ((M + tile - 1) / tile + spare) > kMaxInt / 2) return LQ_ERR_UNSUPPORTED_SHAPE;
+    return launched(lq::launch_int4_mma(p, static_cast<int>(group), tile, stream));
   }
   if ((M + 7) / 8 + spare > 65535) return LQ_ERR_UNSUPPORTED_SHAPE;   // token tiles are the grid's y
   return launched(lq::launch_int4_mm(p, static_cast<int>(group), stream));

@@ -122,7 +122,7 @@ struct Int4Params {
   int num_experts;
   int early_weights;           // stream weights before the grid dependency wait
   int vec_scales;              // a block's scales (and zero points) may be loaded as one aligned word
-  int split;                   // CTAs (a cluster) that share a tile's K (tensor-core kernel)
+  int split;                   // CTAs (a cluster) that share a tile's K, filled by the tensor-core launcher
   int skip_block;              // test hook: >= 0 = the 128-wide K block that is never loaded (tensor-core kernel)
   int* status;                 // device status word
   uint64_t wait_limit_ns;
@@ -139,8 +139,8 @@ int sm_count();        // streaming multiprocessors of the current device
 int int4_mma_max_experts();
 int skipped_block();   // lq_test_inject_stall's K tile, -1 when off
 bool static_weights_declared();
-// The tensor-core kernel: `tile` tokens per tile (16, 32, 64, 128 or 256), K shared by `split` CTAs (a cluster, 1..8).
-cudaError_t launch_int4_mma(const Int4Params& p, int group, int tile, int split, cudaStream_t stream);
+// The tensor-core kernel (int4_mma.cu): `tile` tokens per tile (16, 32, 64, 128 or 256).
+cudaError_t launch_int4_mma(const Int4Params& p, int group, int tile, cudaStream_t stream);
 cudaError_t launch_int4_mm(const Int4Params& p, int group, cudaStream_t stream);
 cudaError_t launch_quant_weight_int4(const void* w, int group, void* q, void* scales, void* zeros, int64_t N,
                                      int64_t K, cudaStream_t stream);

@@ -62,6 +62,7 @@ struct MmaShape {
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kEpiFirst = kTwo ? 2 : 2 + kConvWarps;    // first of the eight epilogue warps
   static_assert(kA * 64 + kD * NT <= kCols, "tensor memory");
+  static_assert(!kTwo || kD == 1, "the converting warps' epilogue knows one accumulator");
 };
 
 constexpr float kSumScale = 1099511627776.f;   // 2^40: taken out of the weights, put back into the sums
@@ -404,9 +405,15 @@ __global__ void __launch_bounds__(MmaShape<NT>::kThreads, MmaShape<NT>::kTwo ? 2
     uint32_t s_phase = 0, b_phase = 1;     // the first kA blocks find their slot free
     const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
     const uint32_t swizzle = (row >> 1) & 3;
-    int k = 0, i = group_id, d = 0;            // tile, block
-    uint32_t d_phase = 0;
+    int k = 0, i = group_id;               // tile, block
+    // With one accumulator and no warps of its own, the epilogue of a tile runs
+    // after this group's first block of the next one: the MMAs of the tile end
+    // meanwhile, and the next tile starts with converted blocks at hand.
+    auto epilogue_of = [&](int tile) {
+      if (ok) epilogue(tile, 0, tile & 1);
+    };
     for (; k < mine && ok; ++k) {
+      bool due = Sh::kTwo && k > 0;
       for (; i < blocks; i += kGroups) {
         uint32_t factor[GB], offset[GB];
 #pragma unroll
@@ -470,16 +477,15 @@ __global__ void __launch_bounds__(MmaShape<NT>::kThreads, MmaShape<NT>::kTwo ? 2
           b -= kA;
           b_phase ^= 1;
         }
-      }
-      i -= blocks;                         // the first block of the next tile that is this group's
-      if constexpr (Sh::kTwo) {
-        if (ok) epilogue(k, d, d_phase);
-        if (++d == kD) {
-          d = 0;
-          d_phase ^= 1;
+        if (due) {
+          epilogue_of(k - 1);
+          due = false;
         }
       }
+      if (due) epilogue_of(k - 1);
+      i -= blocks;                         // the first block of the next tile that is this group's
     }
+    if (Sh::kTwo && mine > 0) epilogue_of(mine - 1);
   }
   if constexpr (!Sh::kTwo) {
     if (warp >= Sh::kEpiFirst) {

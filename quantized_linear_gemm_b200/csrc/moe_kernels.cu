@@ -28,26 +28,41 @@ namespace {
 constexpr int kSortWarps = 32;
 constexpr int kSortThreads = 32 * kSortWarps;
 constexpr int kSortMaxExperts = 1024;   // one scan thread per expert, 4 KB of counts per expert row of a warp
-constexpr int kSortMaxCluster = 8;
+constexpr int kSortMaxCluster = 16;     // more than 8 need the non-portable attribute
 
 // ------------------------------------------------------------------ sort
 //
-// One cluster of up to 8 CTAs does the whole sort in one launch and without
+// One cluster of up to 16 CTAs does the whole sort in one launch and without
 // a workspace.  Each warp owns a contiguous segment of ids and counts it into
 // its own row of shared memory, 32 ids at a time: lanes with the same expert
-// find each other with one match instruction, and one of them adds their
-// number.  Prefix sums over the warps of a CTA, the CTAs of the cluster
+// find each other by one ballot per bit of the expert's number (the match
+// instruction takes time in proportion to the different values, over 1 us with
+// 128 experts), and one of them adds their number.  Prefix sums over the warps of a CTA, the CTAs of the cluster
 // (distributed shared memory) and the experts give every (warp, expert) its
 // first row; a second pass over the segment places the ids.  No two warps
 // share a counter, so the order within an expert is the order of the ids.
+// Latency bound: 64 ids of 128 experts 3.3 us, 4096 6.3 us, 65536 10.8 us (22.6 us
+// with the match instruction and 8 CTAs); one CTA per 1024 ids.
+// lanes whose key, of `bits` bits, is this lane's
+__device__ __forceinline__ uint32_t same_key(int key, int bits) {
+  uint32_t same = 0xffffffffu;
+  for (int b = 0; b < bits; ++b) {
+    const bool one = (key >> b) & 1;
+    const uint32_t v = __ballot_sync(0xffffffffu, one);
+    same &= one ? v : ~v;
+  }
+  return same;
+}
+
 template <typename Id>
 __global__ void __launch_bounds__(kSortThreads) moe_sort_kernel(const Id* __restrict__ ids, int64_t n, int E,
                                                                 int64_t seg, int32_t* __restrict__ offsets,
                                                                 int32_t* __restrict__ order,
                                                                 int32_t* __restrict__ slots) {
   extern __shared__ int32_t sort_smem[];
-  int32_t* counts = sort_smem;                     // [kSortWarps][E]
-  int32_t* cta_total = counts + kSortWarps * E;    // [E], read by the cluster's other CTAs
+  const int stride = E | 1;                        // odd: a column's rows lie in different banks
+  int32_t* counts = sort_smem;                     // [kSortWarps][stride]
+  int32_t* cta_total = counts + kSortWarps * stride;    // [E], read by the cluster's other CTAs
   int32_t* base = cta_total + E;                   // [E] first row of this CTA's ids of each expert
   __shared__ int32_t warp_sum[kSortWarps];
   __shared__ int32_t grand_total;
@@ -55,7 +70,8 @@ __global__ void __launch_bounds__(kSortThreads) moe_sort_kernel(const Id* __rest
   grid_dependency_wait();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int ctas = static_cast<int>(gridDim.x), cta = static_cast<int>(blockIdx.x);
-  int32_t* mine = counts + warp * E;
+  const int bits = 32 - __clz(E);                  // keys 0..E
+  int32_t* mine = counts + warp * stride;
   for (int e = lane; e < E; e += 32) mine[e] = 0;
   __syncwarp();
   const int64_t lo = (static_cast<int64_t>(cta) * kSortWarps + warp) * seg;
@@ -72,24 +88,39 @@ __global__ void __launch_bounds__(kSortThreads) moe_sort_kernel(const Id* __rest
     for (int b = 0; b < kBatch; ++b) key[b] = key_at(i0 + 32 * b + lane);
 #pragma unroll
     for (int b = 0; b < kBatch; ++b) {
-      const uint32_t same = __match_any_sync(0xffffffffu, key[b]);
+      if (i0 + 32 * b >= hi) break;
+      const uint32_t same = same_key(key[b], bits);
       if (key[b] < E && (__ffs(same) - 1) == lane) mine[key[b]] += __popc(same);
       __syncwarp();
     }
   }
   __syncthreads();
-  int total = 0, before = 0;                       // of expert `tid`: rows in the batch, rows in earlier CTAs
-  if (tid < E) {
-    int run = 0;
+  // exclusive prefix over the warps, expert by expert: 8 threads per expert, 4 warps' counts each
+  for (int e0 = 0; e0 < E; e0 += kSortThreads / 8) {
+    const int e = e0 + (tid >> 3), r = tid & 7;
+    int c[4] = {0, 0, 0, 0};
+    if (e < E)
 #pragma unroll
-    for (int w = 0; w < kSortWarps; ++w) {
-      const int c = counts[w * E + tid];
-      counts[w * E + tid] = run;
-      run += c;
+      for (int q = 0; q < 4; ++q) c[q] = counts[(4 * r + q) * stride + e];
+    const int sum = c[0] + c[1] + c[2] + c[3];
+    int upto = sum;
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, upto, o, 8);
+      if (r >= o) upto += v;
     }
-    cta_total[tid] = run;
-    total = run;
+    int run = upto - sum;
+    if (e < E) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        counts[(4 * r + q) * stride + e] = run;
+        run += c[q];
+      }
+      if (r == 7) cta_total[e] = upto;
+    }
   }
+  __syncthreads();
+  int total = tid < E ? cta_total[tid] : 0, before = 0;   // of expert `tid`: rows in the batch, rows in earlier CTAs
   if (ctas > 1) {
     cluster_sync_all();
     if (tid < E) {
@@ -137,7 +168,8 @@ __global__ void __launch_bounds__(kSortThreads) moe_sort_kernel(const Id* __rest
 #pragma unroll
     for (int b = 0; b < kBatch; ++b) {
       const int64_t i = i0 + 32 * b + lane;
-      const uint32_t same = __match_any_sync(0xffffffffu, key[b]);
+      if (i0 + 32 * b >= hi) break;
+      const uint32_t same = same_key(key[b], bits);
       int at = 0;
       if (key[b] < E) at = mine[key[b]];
       __syncwarp();
@@ -320,8 +352,11 @@ __global__ void __launch_bounds__(kRowThreads) moe_unpermute_kernel(const uint4*
 // pieces of dout, writes w dout at every slot and adds up its part of the dot
 // products with the rows of y; the CTA's parts are summed in a fixed order
 // (lanes by shuffles, then the warps in turn).  Eight slots at a time, so dout
-// (in L1 after the first time) is read again only when k > 8.
-constexpr int kBwdThreads = 256;
+// (in L1 after the first time) is read again only when k > 8.  Bound by HBM:
+// 4096 tokens of 8 rows of 2048, 45.4 us, 0.96 of the copy rate (52.5 us with
+// 256 threads per token and cached loads and stores: the barrier of the sum
+// held too many loads back).
+constexpr int kBwdThreads = 128;
 
 __global__ void __launch_bounds__(kBwdThreads) moe_unpermute_backward_kernel(
     const uint4* __restrict__ dout, const uint4* __restrict__ y, const int32_t* __restrict__ slots,
@@ -345,7 +380,7 @@ __global__ void __launch_bounds__(kBwdThreads) moe_unpermute_backward_kernel(
       uint4 r[kSlotBatch];
 #pragma unroll
       for (int j = 0; j < kSlotBatch; ++j)
-        if (row_ok(s[j], P)) r[j] = __ldg(y + static_cast<int64_t>(s[j]) * nvec + v);
+        if (row_ok(s[j], P)) r[j] = __ldcs(y + static_cast<int64_t>(s[j]) * nvec + v);
       float d[8];
       bf16x8_to_f32(__ldg(dout + t * nvec + v), d);
 #pragma unroll
@@ -361,7 +396,7 @@ __global__ void __launch_bounds__(kBwdThreads) moe_unpermute_backward_kernel(
             const __nv_bfloat162 p = __floats2bfloat162_rn(w[j] * d[2 * i], w[j] * d[2 * i + 1]);
             o[i] = *reinterpret_cast<const uint32_t*>(&p);
           }
-          dy[static_cast<int64_t>(s[j]) * nvec + v] = make_uint4(o[0], o[1], o[2], o[3]);
+          __stcs(dy + static_cast<int64_t>(s[j]) * nvec + v, make_uint4(o[0], o[1], o[2], o[3]));
         }
     }
 #pragma unroll
@@ -406,7 +441,7 @@ cudaError_t launch_sort_t(const void* ids, int64_t n, int E, int32_t* offsets, i
   while (ctas < kSortMaxCluster && n > static_cast<int64_t>(ctas) * kSortThreads) ctas *= 2;
   const int64_t warps = static_cast<int64_t>(ctas) * kSortWarps;
   const int64_t seg = (((n + warps - 1) / warps) + 31) / 32 * 32;
-  const size_t smem = sizeof(int32_t) * static_cast<size_t>(E) * (kSortWarps + 2);
+  const size_t smem = sizeof(int32_t) * (static_cast<size_t>(E | 1) * kSortWarps + 2 * static_cast<size_t>(E));
   cudaLaunchAttribute attr[2];
   cudaLaunchConfig_t cfg = pdl_config(dim3(ctas), dim3(kSortThreads), smem, stream, attr);
   attr[1].id = cudaLaunchAttributeClusterDimension;
@@ -417,6 +452,10 @@ cudaError_t launch_sort_t(const void* ids, int64_t n, int E, int32_t* offsets, i
   if (smem > 40 * 1024) {
     const cudaError_t e = cudaFuncSetAttribute(moe_sort_kernel<Id>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+  }
+  if (ctas > 8) {
+    const cudaError_t e = cudaFuncSetAttribute(moe_sort_kernel<Id>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
   }
   return cudaLaunchKernelEx(&cfg, moe_sort_kernel<Id>, static_cast<const Id*>(ids), n, E, seg, offsets, order, slots);

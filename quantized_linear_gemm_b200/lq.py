@@ -529,16 +529,17 @@ def _int4_operands(x, B, b_scales, b_zeros, lead: tuple):
     _need(x, "x", (torch.bfloat16,), 2)
     _need(B, "B", (torch.uint8,), 2 + len(lead))
     M, K = x.shape
-    N = B.shape[-2]
-    if B.shape[-1] * 2 != K:
-        raise ValueError(f"B has {B.shape[-1]} bytes per row, expected K / 2 with K = {K}")
+    *_, N, row = B.shape
+    if row * 2 != K:
+        raise ValueError(f"B has {row} bytes per row, expected K / 2 with K = {K}")
     _need(b_scales, "b_scales", (torch.bfloat16,), 2 + len(lead))
-    groups = b_scales.shape[-1]
+    have = b_scales.shape
+    groups = have[-1]
     if groups == 0 or K % groups or K // groups not in INT4_GROUPS:
         raise ValueError(f"b_scales has {groups} groups per row: K = {K} must hold whole groups of {INT4_GROUPS}")
     want = (*lead, N, groups)
-    if tuple(b_scales.shape) != want:
-        raise ValueError(f"b_scales has shape {tuple(b_scales.shape)}, expected {want}")
+    if have != want:
+        raise ValueError(f"b_scales has shape {tuple(have)}, expected {want}")
     if b_zeros is not None:
         _need(b_zeros, "b_zeros", (torch.uint8,), 2 + len(lead), want)
     return M, N, K, K // groups

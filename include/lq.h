@@ -484,14 +484,15 @@ lq_status lq_quant_weight_int4(const void *w, int64_t group, void *q, void *scal
  *              (or NULL) as above.
  *   bias     : [N] bf16 or NULL, added in fp32 before the rounding.
  *   C        : [M, N] bf16 out, 16-byte aligned.
- *   K        : a positive multiple of group, at most 2^24; N % 8 == 0.
+ *   K        : a positive multiple of group, at most 2^24; N % 8 == 0;
+ *              M < 2^31 - 255.
  *              M == 0 or N == 0 is a no-op.
  * Up to 8 tokens (16 rows of a grouped call) the codes minus the zero points
  * are exact, a group's products are summed in fp32 and then multiplied by the
  * group's scale in fp32; for more tokens, and for few tokens of long or
  * finely grouped rows, the weight (q - z) s is rounded once to bf16 and
- * multiplied on the tensor core with fp32 sums.  |b_scales| < 2^34; sums below
- * 2^-60 in magnitude may lose precision.  No workspace: calls on different
+ * multiplied on the tensor core with fp32 sums.  |b_scales| < 2^34; weights below
+ * 2^-86 and sums below 2^-60 in magnitude may lose precision.  No workspace: calls on different
  * streams may overlap.  Reads B only after the previous kernels on the stream
  * have finished unless lq_declare_static_weights(1) was called.
  * Errors: LQ_ERR_INVALID_ARG, LQ_ERR_ALIGNMENT, LQ_ERR_UNSUPPORTED_SHAPE
@@ -536,8 +537,8 @@ lq_status lq_grouped_int4_mm(const void *x, const void *B, const void *b_scales,
  * when the caller knows a bound), and a slot outside [0, P) is skipped: its
  * row is neither read nor written.  Rows that no slot names are left as they
  * were.  Slots that name a row twice give that row one of the two values.
- * Outputs must not overlap inputs.  H % 8 == 0 (lq_moe_permute_quant: 16), H <= 2^25; rows
- * are dense and 16-byte aligned (codes 8).
+ * Outputs must not overlap inputs.  H % 8 == 0 (lq_moe_permute_quant: 16), H <= 2^25,
+ * k <= 2^24; rows are dense and 16-byte aligned (codes 8).
  *
  * lq_moe_permute: xs[slots[t, j]] = x[t]; x [T, H] bf16, xs [P, H] bf16.  Its
  *   gradient is lq_moe_unpermute with weights NULL.
@@ -659,7 +660,8 @@ lq_status lq_set_trace(uint64_t *device_buffer);
 /*
  * Test hook for failure detection.  While k_tile >= 0, every scaled_mm
  * kernel launched afterwards leaves the k_tile-th K tile of each CTA (every
- * tensor-core 4-bit product: the k_tile-th 128-wide block of K) unloaded, so the tensor-core warp's bounded wait for it runs out: the
+ * tensor-core 4-bit product: the k_tile-th 128-wide block of K) unloaded, so
+ * the tensor-core warp's bounded wait for it runs out: the
  * kernel sets the device status word, drains its copies, frees its tensor
  * memory and returns (C undefined), and lq_device_status reports
  * LQ_ERR_DEVICE_TIMEOUT.  Nothing faults or hangs.  wait_limit_ns > 0

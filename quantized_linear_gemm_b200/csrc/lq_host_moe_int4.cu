@@ -55,7 +55,9 @@ lq_status int4_mm_impl(const void* x, const void* B, const void* scales, const v
       (offsets && !aligned(offsets, 4)))
     return LQ_ERR_ALIGNMENT;
   if (K == 0 || K % group != 0 || N % 8 != 0) return LQ_ERR_UNSUPPORTED_SHAPE;
-  if (M > kMaxInt || K > (int64_t(1) << 24) || E > kMaxInt || N > kMaxInt || E * N > kMaxInt) return LQ_ERR_UNSUPPORTED_SHAPE;
+  // the kernels round M up to a token tile in 32 bits
+  if (M > kMaxInt - 255 || K > (int64_t(1) << 24) || E > kMaxInt || N > kMaxInt || E * N > kMaxInt)
+    return LQ_ERR_UNSUPPORTED_SHAPE;
   lq::Int4Params p{};
   p.x = static_cast<const __nv_bfloat16*>(x);
   p.B = static_cast<const uint8_t*>(B);
@@ -87,7 +89,7 @@ lq_status int4_mm_impl(const void* x, const void* B, const void* scales, const v
 // Shared checks of the row movements: T tokens of k slots, rows of H values.
 lq_status check_rows(int64_t T, int64_t P, int64_t k, int64_t H, int64_t multiple) {
   if (T < 0 || P < 0 || k < 0 || H < 0) return LQ_ERR_INVALID_ARG;
-  if (H % multiple != 0 || T > kMaxInt || k > kMaxInt || P > kMaxInt || H > (int64_t(1) << 25))
+  if (H % multiple != 0 || T > kMaxInt || k > (int64_t(1) << 24) || P > kMaxInt || H > (int64_t(1) << 25))
     return LQ_ERR_UNSUPPORTED_SHAPE;
   return LQ_OK;
 }

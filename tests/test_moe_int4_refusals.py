@@ -237,3 +237,16 @@ def test_c_grouped_int4_mm(args, want):
 ])
 def test_c_refusals(name, args, want):
     assert lq.call_raw(name, *args) == want
+
+
+@pytest.mark.parametrize("name,args", [
+    ("lq_int4_mm", (A, A, A, None, None, A, (1 << 31) - 255, 8, 32, 32, None)),       # rounded up to a tile: 2^31
+    ("lq_int4_mm", (A, A, A, None, None, A, 4, 8, (1 << 24) + 32, 32, None)),
+    ("lq_grouped_int4_mm", (A, A, A, None, A, A, 2, (1 << 31) - 255, 8, 32, 32, None)),
+    ("lq_moe_permute", (A, A, A, 1, 8, (1 << 31) - 1, 16, None)),                     # slots counted in steps of 8
+    ("lq_moe_permute_quant", (0, A, A, A, A, 1, 8, (1 << 31) - 1, 16, None)),
+    ("lq_moe_unpermute", (A, A, None, A, 1, 8, (1 << 24) + 1, 16, None)),
+    ("lq_moe_unpermute_backward", (A, A, A, A, A, A, 1, 8, (1 << 24) + 1, 16, None)),
+])
+def test_c_counts_past_32_bits(name, args):
+    assert lq.call_raw(name, *args) == SHAPE

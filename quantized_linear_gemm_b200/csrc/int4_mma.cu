@@ -321,8 +321,8 @@ __global__ void __launch_bounds__(MmaShape<NT>::kThreads, MmaShape<NT>::kTwo ? 2
         else tmem_ld_32x32b_x8(at + c, r);
         tmem_ld_wait();
 #pragma unroll
-        for (int j = 0; j < kChunk; ++j)   // a rank without blocks has no sums
-          sums[(c0 + c + j) * 128 + quad * 32 + lane] = blocks > 0 ? __uint_as_float(r[j]) * kSumScale : 0.f;
+        for (int j = 0; j < kChunk; ++j)
+          sums[(c0 + c + j) * 128 + quad * 32 + lane] = __uint_as_float(r[j]) * kSumScale;
       }
       return;
     }
@@ -393,14 +393,12 @@ __global__ void __launch_bounds__(MmaShape<NT>::kThreads, MmaShape<NT>::kTwo ? 2
       }
       load_scales();
     };
-    if (blocks > 0) {
-      while (sc_block >= blocks) {
-        sc_block -= blocks;
-        ++sc_tile;
-      }
-      if (sc_tile < mine) enter_tile();
-      load_scales();
+    while (sc_block >= blocks) {
+      sc_block -= blocks;
+      ++sc_tile;
     }
+    if (sc_tile < mine) enter_tile();
+    load_scales();
     int s = group_id % kRing, b = group_id;        // ring slot and converted-block slot
     uint32_t s_phase = 0, b_phase = 1;     // the first kA blocks find their slot free
     const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
@@ -590,21 +588,32 @@ cudaError_t launch_mma_gn(const Int4Params& params, cudaStream_t stream) {
   const bool zeros = p.zeros != nullptr;
   auto kernel = zeros ? int4_mma_kernel<G, NT, true> : int4_mma_kernel<G, NT, false>;
   static std::atomic<uint64_t> prepared[2];   // devices (by bit) whose kernel has its attributes, per kZeros
+  static std::atomic<int> smem_bytes[2];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   const uint64_t bit = uint64_t(1) << (dev & 63);
   if (!(prepared[zeros].load() & bit)) {
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kSmem);
+    // Half an SM's shared memory exactly (228 KB, 1 KB reserved per CTA) where two CTAs run side by
+    // side: then no CTA that allocates all tensor-memory columns fits beside one (those of this library
+    // take more than half), and CTAs of clusters never wait for columns held by each other's peers.
+    cudaFuncAttributes attributes;
+    e = cudaFuncGetAttributes(&attributes, kernel);
+    if (e != cudaSuccess) return e;
+    const int half = 114 * 1024 - 1024 - static_cast<int>(attributes.sharedSizeBytes);
+    const int bytes = Sh::kTwo ? half : Sh::kSmem;
+    if (bytes < Sh::kSmem) return cudaErrorInvalidConfiguration;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     // without it the driver may size the shared memory for one CTA per SM
     if (e == cudaSuccess)
       e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
     if (e != cudaSuccess) return e;
+    smem_bytes[zeros].store(bytes);
     prepared[zeros].fetch_or(bit);
   }
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(Sh::kThreads);
-  cfg.dynamicSmemBytes = Sh::kSmem;
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem_bytes[zeros].load());
   cfg.stream = stream;
 
   // Split-K: few tiles, each shared by a cluster of as many CTAs as find an SM

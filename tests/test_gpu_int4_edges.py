@@ -185,6 +185,33 @@ def test_two_graphs_at_once(cuda_device):
     assert lq.device_status(0) == 0
 
 
+@pytest.mark.parametrize("fmt", ["fp8_dynamic", "block_fp8"])
+def test_beside_an_8_bit_product(cuda_device, fmt):
+    """Split-K clusters of both kinds of product on two streams: neither waits for tensor memory of the other's
+    cluster peers for good, and no result changes."""
+    x = inputs.activations(64, 8192, seed=1).cuda()
+    B, s, _ = weight(512, 8192, 128, False, 3)
+    B, s = dev(B), dev(s, torch.bfloat16)
+    w = inputs.weights(1024, 8192, seed=4).cuda()
+    if fmt == "block_fp8":
+        a, sa = lq.quant_per_token_group128(x)
+        b, sb = lq.quant_weight_block128(w)
+    else:
+        a, sa = lq.quant_per_token(fmt, x)
+        b, sb = lq.quant_per_token(fmt, w)
+    r4, r8 = lq.int4_mm(x, B, s), lq.scaled_mm(fmt, a, sa, b, sb)
+    torch.cuda.synchronize()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    for _ in range(20):
+        with torch.cuda.stream(s1):
+            c4 = [lq.int4_mm(x, B, s) for _ in range(5)]
+        with torch.cuda.stream(s2):
+            c8 = [lq.scaled_mm(fmt, a, sa, b, sb) for _ in range(5)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(c, r4) for c in c4) and all(torch.equal(c, r8) for c in c8)
+    assert lq.device_status(0) == 0
+
+
 @pytest.mark.parametrize("M", [4, 40, 300])
 def test_weight_written_just_before(cuda_device, M):
     """A weight quantized on the same stream right before the product is the one used, whatever was there."""

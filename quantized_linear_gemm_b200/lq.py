@@ -591,10 +591,11 @@ def moe_sort(topk_ids: torch.Tensor, num_experts: int, expert_offsets=None, orde
     _need(topk_ids, "topk_ids", (torch.int32, torch.int64), 2)
     T, k = topk_ids.shape
     E, n = int(num_experts), T * k
-    if expert_offsets is None and order is None and slots is None:   # one allocation, three views
-        buf = topk_ids.new_empty(max(E, 0) + 1 + 2 * n, dtype=torch.int32)
-        outs = [buf.as_strided((max(E, 0) + 1,), (1,), 0), buf.as_strided((n,), (1,), max(E, 0) + 1),
-                buf.as_strided((T, k), (k, 1), max(E, 0) + 1 + n)]
+    if expert_offsets is None and order is None and slots is None and E >= 0:   # one allocation, cut in three
+        buf = topk_ids.new_empty(E + 1 + 2 * n, dtype=torch.int32)
+        offs, rows, cut = torch.unsafe_split_with_sizes(buf, (E + 1, n, n))
+        outs = (offs, rows, cut.view(T, k))
+        _one_device(topk_ids)
     else:
         outs = []
         for name, t, shape in (("expert_offsets", expert_offsets, (E + 1,)), ("order", order, (n,)),
@@ -604,7 +605,7 @@ def moe_sort(topk_ids: torch.Tensor, num_experts: int, expert_offsets=None, orde
             else:
                 _need(t, name, (torch.int32,), len(shape), shape)
             outs.append(t)
-    _one_device(topk_ids, *outs)
+        _one_device(topk_ids, *outs)
     _check("lq_moe_sort", lib().lq_moe_sort(_ptr(topk_ids), topk_ids.element_size(), n, E, *map(_ptr, outs),
                                             _stream(stream)))
     return tuple(outs)

@@ -37,12 +37,13 @@ constexpr int kSortMaxCluster = 16;     // more than 8 need the non-portable att
 // its own row of shared memory, 32 ids at a time: lanes with the same expert
 // find each other by one ballot per bit of the expert's number (the match
 // instruction takes time in proportion to the different values, over 1 us with
-// 128 experts), and one of them adds their number.  Prefix sums over the warps of a CTA, the CTAs of the cluster
-// (distributed shared memory) and the experts give every (warp, expert) its
-// first row; a second pass over the segment places the ids.  No two warps
+// 128 experts), and one of them adds their number.  Prefix sums over the warps
+// of a CTA, the CTAs of the cluster (distributed shared memory) and the experts
+// give every (warp, expert) its first row; a second pass over the segment places the ids.  No two warps
 // share a counter, so the order within an expert is the order of the ids.
 // Latency bound: 64 ids of 128 experts 3.3 us, 4096 6.3 us, 65536 10.8 us (22.6 us
 // with the match instruction and 8 CTAs); one CTA per 1024 ids.
+
 // lanes whose key, of `bits` bits, is this lane's
 __device__ __forceinline__ uint32_t same_key(int key, int bits) {
   uint32_t same = 0xffffffffu;
@@ -195,7 +196,8 @@ __global__ void __launch_bounds__(kSortThreads) moe_sort_kernel(const Id* __rest
 //
 // One thread holds one 16-byte piece of a token's row and stores it at each of
 // the token's slots: x is read once and every copy written once.  Bound by
-// the writes.
+// the writes: 4096 tokens of 2048 values at 8 slots 25.3 us, 0.91 of the copy
+// rate; 32 tokens 1.5 us, the launch.
 constexpr int kRowThreads = 128;
 constexpr int kSlotBatch = 8;   // slots (and, in the sums, rows) in flight per thread
 
@@ -225,7 +227,9 @@ __global__ void __launch_bounds__(kRowThreads) moe_permute_kernel(const uint4* _
 // ... with the per-token quantization of quant_kernels.cu: one CTA per token,
 // the row in registers (VPT pieces of 8 values per thread; VPT = 0: longer
 // rows, read twice), its codes stored at each slot.  Same codes and scales,
-// bit for bit, as quantizing x first.
+// bit for bit, as quantizing x first.  Bound by the writes at many tokens, by
+// the row's maximum before them at fewer: 8192 tokens of 2048 values at 8 slots
+// 29.4 us, 0.87 of the copy rate, 4096 tokens 16.2 us, 0.79; 32 tokens 1.8 us.
 constexpr int kQuantThreads = 256;
 
 __device__ __forceinline__ float block_max_256(float v, float* red) {
@@ -306,7 +310,9 @@ __global__ void __launch_bounds__(kQuantThreads) moe_permute_quant_kernel(const 
 // One thread sums one 16-byte piece over the token's rows, in the order
 // j = 0..k-1 in fp32, and rounds once to bf16.  Up to eight rows are in
 // flight per thread.  A row whose slot is outside [0, P) is not read, so
-// whatever it would hold (NaN included) cannot reach the sum.
+// whatever it would hold (NaN included) cannot reach the sum.  Bound by the
+// reads: 4096 tokens of 8 rows of 2048 values 25.3 us, 0.91 of the copy rate;
+// 32 tokens 2.1 us, the launch and two dependent loads.
 __global__ void __launch_bounds__(kRowThreads) moe_unpermute_kernel(const uint4* __restrict__ y,
                                                                     const int32_t* __restrict__ slots,
                                                                     const float* __restrict__ weights,

@@ -381,16 +381,38 @@ __global__ void __launch_bounds__(MmaShape<NT>::kThreads, MmaShape<NT>::kTwo ? 2
       sr = p.scales + w * groups;
       zr = kZeros ? p.zeros + w * groups : nullptr;
     };
-    __nv_bfloat16 s_next[GB];
-    uint8_t z_next[GB];
+    // of a block's groups, packed as they lie in memory and taken apart at their use: a load whose result
+    // is unpacked where two ways of loading meet would be waited for there.  One load instead of one per
+    // group: [24576, 4096], 64 tokens, G = 32 with zero points 55 -> 33 us; [5120, 25600], 37 tokens, G = 64
+    // with zero points 35.7 -> 31.6 us.
+    uint32_t s_next[(GB + 1) / 2], z_next = 0;
     auto load_scales = [&] {
       if (sc_tile >= mine) return;
       const int at = (kb_lo + sc_block) * GB;
+      if constexpr (GB == 1) {
+        s_next[0] = __bfloat16_as_ushort(__ldg(sr + at));
+        if (kZeros) z_next = __ldg(zr + at);
+        return;
+      }
+      if (p.vec_scales) {                  // in one load each
+        if constexpr (GB == 4) {
+          const uint2 v = __ldg(reinterpret_cast<const uint2*>(sr + at));
+          s_next[0] = v.x;
+          s_next[GB / 2 - 1] = v.y;
+          if (kZeros) z_next = __ldg(reinterpret_cast<const uint32_t*>(zr + at));
+        } else {
+          s_next[0] = __ldg(reinterpret_cast<const uint32_t*>(sr + at));
+          if (kZeros) z_next = __ldg(reinterpret_cast<const uint16_t*>(zr + at));
+        }
+        return;
+      }
+      z_next = 0;
 #pragma unroll
       for (int j = 0; j < GB; ++j) {
-        const int a = GB == 1 || at + j < groups ? at + j : groups - 1;   // past K: the activations are zero
-        s_next[j] = __ldg(sr + a);
-        if (kZeros) z_next[j] = __ldg(zr + a);
+        const int a = at + j < groups ? at + j : groups - 1;   // past K: the activations are zero
+        const uint32_t v = __bfloat16_as_ushort(__ldg(sr + a));
+        s_next[j / 2] = j & 1 ? s_next[j / 2] | v << 16 : v;
+        if (kZeros) z_next |= static_cast<uint32_t>(__ldg(zr + a)) << (8 * j);
       }
     };
     auto next_scales = [&] {               // this group's next block
@@ -427,10 +449,10 @@ __global__ void __launch_bounds__(MmaShape<NT>::kThreads, MmaShape<NT>::kTwo ? 2
         uint32_t factor[GB], offset[GB];
 #pragma unroll
         for (int j = 0; j < GB; ++j) {
-          const float sf = __bfloat162float(s_next[j]);
+          const float sf = __uint_as_float(j & 1 ? s_next[j / 2] & 0xFFFF0000u : s_next[j / 2] << 16);   // bf16
           if constexpr (kZeros) {
             factor[j] = bf16x2_same(sf * 0x1p-34f);      // of (q - z) / 64
-            offset[j] = int4_offset(z_next[j]);
+            offset[j] = int4_offset(z_next >> (8 * j));
           } else {
             factor[j] = scale_factors(sf);
             offset[j] = bf16x2_same(sf * -0x1p-37f);     // -8 s 2^-40

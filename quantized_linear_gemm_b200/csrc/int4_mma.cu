@@ -39,42 +39,14 @@
 #include <cstdint>
 
 #include "int4_common.cuh"
+#include "int4_mma_shape.h"
 #include "lq_kernels.h"
 #include "ptx.cuh"
 
 namespace lq {
 namespace {
 
-constexpr int kMaxRing = 8, kMaxA = 4;
-constexpr int kWeightTile = 128 * 64;   // bytes of a 128-row, 128-wide block of codes
 constexpr int kMaxGroupedExperts = 1024;
-
-// NT <= 64: two CTAs per SM, one accumulator, the converting warps also run
-// the epilogue (the other CTA computes meanwhile, and the next launch fits
-// beside this one).  Larger tiles: one CTA per SM and eight epilogue warps; at
-// 128 tokens two accumulators, at 256 the accumulator and four converted
-// blocks fill the tensor memory.
-template <int NT>
-struct MmaShape {
-  static constexpr int kTokenTile = NT * 256;                    // bytes of NT tokens x 128 k
-  static constexpr int kStage = kWeightTile + kTokenTile;
-  static constexpr bool kTwo = NT <= 64;
-  static constexpr int kFit = (kTwo ? 100 : 217) * 1024 / kStage;
-  static constexpr int kRing = kFit < kMaxRing ? kFit : kMaxRing;
-  static constexpr int kA = kTwo ? 3 : 4;                        // converted weight blocks in tensor memory
-  static constexpr int kD = NT == 128 ? 2 : 1;                   // accumulators
-  static constexpr int kCols = kTwo ? 256 : 512;                 // tensor-memory columns
-  static constexpr int kSmem = kRing * kStage + 1024;
-  // converting groups of four warps, group g takes blocks g, g + kGroups, ...; one keeps up with the
-  // MMAs of 256 tokens, and with 14 warps the epilogue has the registers for its packed columns
-  static constexpr int kGroups = NT == 256 ? 1 : 2;
-  static constexpr int kConvWarps = 4 * kGroups;
-  static constexpr int kWarps = 2 + kConvWarps + (kTwo ? 0 : 8);
-  static constexpr int kThreads = 32 * kWarps;
-  static constexpr int kEpiFirst = kTwo ? 2 : 2 + kConvWarps;    // first of the eight epilogue warps
-  static_assert(kA * 64 + kD * NT <= kCols, "tensor memory");
-  static_assert(!kTwo || kD == 1, "the converting warps' epilogue knows one accumulator");
-};
 
 constexpr float kSumScale = 1099511627776.f;   // 2^40: taken out of the weights, put back into the sums
 

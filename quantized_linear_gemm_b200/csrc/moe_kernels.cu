@@ -16,6 +16,7 @@
 // sum has a fixed order, so results are reproducible bit for bit.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
+#include <atomic>
 #include <cstdint>
 
 #include "lq_kernels.h"
@@ -440,6 +441,29 @@ dim3 row_grid(int64_t T, int64_t nvec) {
   return dim3(static_cast<unsigned>(T), static_cast<unsigned>((nvec + kRowThreads - 1) / kRowThreads));
 }
 
+constexpr size_t sort_smem_bytes(int E) {
+  return sizeof(int32_t) * (static_cast<size_t>(E | 1) * kSortWarps + 2 * static_cast<size_t>(E));
+}
+
+// The kernel's limits, set once per device to what the most experts need: a
+// limit that followed each call's E would be lowered by one host thread between
+// another's setting and its launch.
+template <typename Id>
+cudaError_t prepare_sort() {
+  static std::atomic<uint64_t> prepared;   // devices, by bit
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = uint64_t(1) << (dev & 63);
+  if (prepared.load() & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(moe_sort_kernel<Id>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           static_cast<int>(sort_smem_bytes(kSortMaxExperts)));
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(moe_sort_kernel<Id>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e == cudaSuccess) prepared.fetch_or(bit);
+  return e;
+}
+
 template <typename Id>
 cudaError_t launch_sort_t(const void* ids, int64_t n, int E, int32_t* offsets, int32_t* order, int32_t* slots,
                           cudaStream_t stream) {
@@ -447,23 +471,15 @@ cudaError_t launch_sort_t(const void* ids, int64_t n, int E, int32_t* offsets, i
   while (ctas < kSortMaxCluster && n > static_cast<int64_t>(ctas) * kSortThreads) ctas *= 2;
   const int64_t warps = static_cast<int64_t>(ctas) * kSortWarps;
   const int64_t seg = (((n + warps - 1) / warps) + 31) / 32 * 32;
-  const size_t smem = sizeof(int32_t) * (static_cast<size_t>(E | 1) * kSortWarps + 2 * static_cast<size_t>(E));
+  const cudaError_t e = prepare_sort<Id>();
+  if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[2];
-  cudaLaunchConfig_t cfg = pdl_config(dim3(ctas), dim3(kSortThreads), smem, stream, attr);
+  cudaLaunchConfig_t cfg = pdl_config(dim3(ctas), dim3(kSortThreads), sort_smem_bytes(E), stream, attr);
   attr[1].id = cudaLaunchAttributeClusterDimension;
   attr[1].val.clusterDim.x = ctas;
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cfg.numAttrs = 2;
-  if (smem > 40 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(moe_sort_kernel<Id>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               static_cast<int>(smem));
-    if (e != cudaSuccess) return e;
-  }
-  if (ctas > 8) {
-    const cudaError_t e = cudaFuncSetAttribute(moe_sort_kernel<Id>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e != cudaSuccess) return e;
-  }
   return cudaLaunchKernelEx(&cfg, moe_sort_kernel<Id>, static_cast<const Id*>(ids), n, E, seg, offsets, order, slots);
 }
 

@@ -20,16 +20,14 @@
 #include <cstdint>
 
 #include "lq_kernels.h"
+#include "moe_sort_shape.h"
 #include "ptx.cuh"
 #include "quant_common.cuh"
 
 namespace lq {
 namespace {
 
-constexpr int kSortWarps = 32;
-constexpr int kSortThreads = 32 * kSortWarps;
 constexpr int kSortMaxExperts = 1024;   // one scan thread per expert, 4 KB of counts per expert row of a warp
-constexpr int kSortMaxCluster = 16;     // more than 8 need the non-portable attribute
 
 // ------------------------------------------------------------------ sort
 //
@@ -447,40 +445,59 @@ constexpr size_t sort_smem_bytes(int E) {
 
 // The kernel's limits, set once per device to what the most experts need: a
 // limit that followed each call's E would be lowered by one host thread between
-// another's setting and its launch.
+// another's setting and its launch.  With them the widest cluster: 16 CTAs where
+// the device has room for one with that much shared memory, else 8, which every
+// device takes.
 template <typename Id>
-cudaError_t prepare_sort() {
-  static std::atomic<uint64_t> prepared;   // devices, by bit
+cudaError_t prepare_sort(int* widest) {
+  static std::atomic<int> prepared[64];   // per device: the widest cluster, 0 before the first call
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  const uint64_t bit = uint64_t(1) << (dev & 63);
-  if (prepared.load() & bit) return cudaSuccess;
-  e = cudaFuncSetAttribute(moe_sort_kernel<Id>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           static_cast<int>(sort_smem_bytes(kSortMaxExperts)));
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(moe_sort_kernel<Id>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-  if (e == cudaSuccess) prepared.fetch_or(bit);
-  return e;
+  std::atomic<int>& slot = prepared[dev & 63];
+  *widest = slot.load();
+  if (*widest) return cudaSuccess;
+  constexpr size_t most = sort_smem_bytes(kSortMaxExperts);
+  e = cudaFuncSetAttribute(moe_sort_kernel<Id>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(most));
+  if (e != cudaSuccess) return e;
+  int fitting = 0;
+  e = cudaFuncSetAttribute(moe_sort_kernel<Id>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e == cudaSuccess) {
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = kSortMaxCluster;
+    attr.val.clusterDim.y = 1;
+    attr.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(kSortMaxCluster);
+    cfg.blockDim = dim3(kSortThreads);
+    cfg.dynamicSmemBytes = most;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    e = cudaOccupancyMaxActiveClusters(&fitting, moe_sort_kernel<Id>, &cfg);
+  }
+  if (e != cudaSuccess) cudaGetLastError();
+  *widest = sort_widest(static_cast<int>(e), fitting);
+  slot.store(*widest);
+  return cudaSuccess;
 }
 
 template <typename Id>
 cudaError_t launch_sort_t(const void* ids, int64_t n, int E, int32_t* offsets, int32_t* order, int32_t* slots,
                           cudaStream_t stream) {
-  int ctas = 1;
-  while (ctas < kSortMaxCluster && n > static_cast<int64_t>(ctas) * kSortThreads) ctas *= 2;
-  const int64_t warps = static_cast<int64_t>(ctas) * kSortWarps;
-  const int64_t seg = (((n + warps - 1) / warps) + 31) / 32 * 32;
-  const cudaError_t e = prepare_sort<Id>();
+  int widest = 0;
+  const cudaError_t e = prepare_sort<Id>(&widest);
   if (e != cudaSuccess) return e;
+  const SortShape shape = sort_shape(n, widest);
   cudaLaunchAttribute attr[2];
-  cudaLaunchConfig_t cfg = pdl_config(dim3(ctas), dim3(kSortThreads), sort_smem_bytes(E), stream, attr);
+  cudaLaunchConfig_t cfg = pdl_config(dim3(shape.ctas), dim3(kSortThreads), sort_smem_bytes(E), stream, attr);
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = ctas;
+  attr[1].val.clusterDim.x = shape.ctas;
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, moe_sort_kernel<Id>, static_cast<const Id*>(ids), n, E, seg, offsets, order, slots);
+  return cudaLaunchKernelEx(&cfg, moe_sort_kernel<Id>, static_cast<const Id*>(ids), n, E, shape.seg, offsets,
+                            order, slots);
 }
 
 }  // namespace

@@ -684,9 +684,10 @@ def moe_permute_backward(dxs: torch.Tensor, slots: torch.Tensor, dx: torch.Tenso
 def moe_unpermute_backward(dout: torch.Tensor, y: torch.Tensor, slots: torch.Tensor, weights: torch.Tensor,
                            dy: torch.Tensor | None = None, dweights: torch.Tensor | None = None, stream=None):
     """``lq_moe_unpermute_backward``: (dy bf16 [P, H], dweights fp32 [T, k]) of
-    moe_unpermute(y, slots, weights) for the gradient dout bf16 [T, H]; rows of
-    dy that no slot names are left as they were.  (Without weights the gradient
-    is moe_permute(dout, slots).)"""
+    moe_unpermute(y, slots, weights) for the gradient dout bf16 [T, H].  Rows
+    that no slot names have gradient zero in a dy allocated here; in the
+    caller's dy they are left as they were, which saves clearing it.  (Without
+    weights the gradient is moe_permute(dout, slots, xs=zeros).)"""
     _need(y, "y", (torch.bfloat16,), 2)
     _need(slots, "slots", (torch.int32,), 2)
     P, H = y.shape
@@ -694,7 +695,7 @@ def moe_unpermute_backward(dout: torch.Tensor, y: torch.Tensor, slots: torch.Ten
     _need(dout, "dout", (torch.bfloat16,), 2, (T, H))
     _need(weights, "weights", (torch.float32,), 2, (T, k))
     if dy is None:
-        dy = y.new_empty((P, H))
+        dy = y.new_zeros((P, H))
     else:
         _need(dy, "dy", (torch.bfloat16,), 2, (P, H))
     if dweights is None:

@@ -142,14 +142,19 @@ __global__ void __launch_bounds__(32 * W) int4_stream_kernel(const Int4Params p)
   grid_launch_dependents();
   const int K = static_cast<int>(p.K), groups = K / G, blocks = (K + 127) / 128;
   const int M = static_cast<int>(p.M);
-  int m0 = static_cast<int>(blockIdx.y) * kTokens, m1 = m0 + kTokens < M ? m0 + kTokens : M;
+  const int tile = static_cast<int>(blockIdx.z * gridDim.y + blockIdx.y);   // of kTokens tokens
+  int m0 = 0, m1 = 0;
   int64_t first_row = static_cast<int64_t>(blockIdx.x) * kRows;
   const int rows_left = static_cast<int>(p.N - first_row < kRows ? p.N - first_row : kRows);
   grid_dependency_wait();
   if (p.expert_offsets) {
     int expert;
-    if (!find_expert_tile(p.expert_offsets, p.num_experts, M, kTokens, blockIdx.y, &expert, &m0, &m1)) return;
+    if (!find_expert_tile(p.expert_offsets, p.num_experts, M, kTokens, tile, &expert, &m0, &m1)) return;
     first_row += expert * p.N;
+  } else {
+    m0 = tile * kTokens;
+    if (m0 >= M) return;
+    m1 = m0 + kTokens < M ? m0 + kTokens : M;
   }
   const int toks_left = m1 - m0;
 
@@ -291,9 +296,10 @@ cudaError_t launch_stream_gmr(const Int4Params& p, cudaStream_t stream) {
   const int64_t gx = (p.N + kRows - 1) / kRows;
   int64_t gy = (p.M + kTokens - 1) / kTokens;
   if (p.expert_offsets) gy += p.num_experts < p.M ? p.num_experts : p.M;
-  if (gy > 65535) return cudaErrorInvalidValue;
+  const int64_t gz = (gy + 65534) / 65535;               // token tiles over y and z; those past the last one return
+  gy = (gy + gz - 1) / gz;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(gx), static_cast<unsigned>(gy));
+  cfg.gridDim = dim3(static_cast<unsigned>(gx), static_cast<unsigned>(gy), static_cast<unsigned>(gz));
   cfg.blockDim = dim3(32 * W);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];

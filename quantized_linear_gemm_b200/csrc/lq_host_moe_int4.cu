@@ -77,12 +77,11 @@ lq_status int4_mm_impl(const void* x, const void* B, const void* scales, const v
   if (rc != LQ_OK) return static_cast<lq_status>(rc);
   p.skip_block = lq::skipped_block();
   const int tile = tensor_tile(M, N, K, group, grouped ? E : 0);
-  const int64_t spare = grouped ? (E < M ? E : M) : 0;       // token tiles beyond M / tile, at most
   if (tile) {
+    const int64_t spare = grouped ? (E < M ? E : M) : 0;     // token tiles beyond M / tile, at most
     if (((N + 127) / 128) * ((M + tile - 1) / tile + spare) > kMaxInt / 2) return LQ_ERR_UNSUPPORTED_SHAPE;
     return launched(lq::launch_int4_mma(p, static_cast<int>(group), tile, stream));
   }
-  if ((M + 7) / 8 + spare > 65535) return LQ_ERR_UNSUPPORTED_SHAPE;   // token tiles are the grid's y
   return launched(lq::launch_int4_mm(p, static_cast<int>(group), stream));
 }
 

@@ -311,20 +311,19 @@ cudaError_t launch_stream_gmr(const Int4Params& p, cudaStream_t stream) {
                  : cudaLaunchKernelEx(&cfg, int4_stream_kernel<G, MT, RT, W, false>, p);
 }
 
-// 16-row tiles with 16 warps per tile until there are enough rows to fill the
-// GPU with 32-row tiles of 8 warps.  Measured on B200, one token, G = 128:
-// [4096, 4096] 4.7 us with 16 rows / 16 warps, 8.0 us with 32 / 8; [4096, 12288]
-// 9.8 and 20.0; [24576, 4096] 18.9 and 15.5.
-template <int G, int MT>
-cudaError_t launch_stream_gm(const Int4Params& p, cudaStream_t stream) {
-  const bool many = p.expert_offsets || p.N >= 16384;   // a grouped product has tiles of many experts
-  return many ? launch_stream_gmr<G, MT, 2, 8>(p, stream) : launch_stream_gmr<G, MT, 1, 16>(p, stream);
-}
-
+// Dense (at most 8 tokens): 16-row tiles with 16 warps per tile until there are
+// enough rows to fill the GPU with 32-row tiles of 8 warps.  Measured on B200,
+// one token, G = 128: [4096, 4096] 4.7 us with 16 rows / 16 warps, 8.0 us with
+// 32 / 8; [4096, 12288] 9.8 and 20.0; [24576, 4096] 18.9 and 15.5.  Grouped:
+// the tiles of many experts are enough rows; two 8-token tiles per CTA where
+// the experts have more than 8 rows on average (more than 1024 experts: fewer
+// take the tensor-core kernel).
 template <int G>
 cudaError_t launch_stream_g(const Int4Params& p, cudaStream_t stream) {
-  const int64_t per = p.expert_offsets ? (p.M + p.num_experts - 1) / p.num_experts : p.M;   // tokens per product
-  return per <= 8 ? launch_stream_gm<G, 1>(p, stream) : launch_stream_gm<G, 2>(p, stream);
+  if (!p.expert_offsets)
+    return p.N >= 16384 ? launch_stream_gmr<G, 1, 2, 8>(p, stream) : launch_stream_gmr<G, 1, 1, 16>(p, stream);
+  const int64_t per = (p.M + p.num_experts - 1) / p.num_experts;
+  return per <= 8 ? launch_stream_gmr<G, 1, 2, 8>(p, stream) : launch_stream_gmr<G, 2, 2, 8>(p, stream);
 }
 
 template <int G>

@@ -170,6 +170,17 @@ def _stream(stream=None) -> int:
     return int(stream.cuda_stream)
 
 
+def _zeros(like: torch.Tensor, shape, stream=None) -> torch.Tensor:
+    """Zeros of like's type, cleared on the stream that the call runs on: on
+    another one the clearing could come after the kernel's stores."""
+    if stream is None or not like.is_cuda:
+        return like.new_zeros(shape)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream.cuda_stream), device=like.device)
+    with torch.cuda.stream(stream):
+        return like.new_zeros(shape)
+
+
 def _fmt(fmt) -> int:
     if isinstance(fmt, str):
         return FORMATS[fmt]
@@ -695,7 +706,7 @@ def moe_unpermute_backward(dout: torch.Tensor, y: torch.Tensor, slots: torch.Ten
     _need(dout, "dout", (torch.bfloat16,), 2, (T, H))
     _need(weights, "weights", (torch.float32,), 2, (T, k))
     if dy is None:
-        dy = y.new_zeros((P, H))
+        dy = _zeros(y, (P, H), stream)
     else:
         _need(dy, "dy", (torch.bfloat16,), 2, (P, H))
     if dweights is None:

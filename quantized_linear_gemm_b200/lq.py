@@ -170,15 +170,24 @@ def _stream(stream=None) -> int:
     return int(stream.cuda_stream)
 
 
-def _zeros(like: torch.Tensor, shape, stream=None) -> torch.Tensor:
-    """Zeros of like's type, cleared on the stream that the call runs on: on
-    another one the clearing could come after the kernel's stores."""
+def _alloc(like: torch.Tensor, shape, stream=None, dtype=None, zero: bool = False) -> torch.Tensor:
+    """A new output beside `like`, from the memory of the stream that the call
+    runs on (and cleared there): memory of another stream may still be in use
+    by work queued on that one, and clearing there could come after the
+    kernel's stores.  The caller's current stream is noted as a user, so that a
+    dropped output is not handed out again before what was queued there."""
+    make = like.new_zeros if zero else like.new_empty
+    dtype = like.dtype if dtype is None else dtype
     if stream is None or not like.is_cuda:
-        return like.new_zeros(shape)
+        return make(shape, dtype=dtype)
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(int(stream.cuda_stream), device=like.device)
+    current = torch.cuda.current_stream()
     with torch.cuda.stream(stream):
-        return like.new_zeros(shape)
+        out = make(shape, dtype=dtype)
+    if current.cuda_stream != stream.cuda_stream:
+        out.record_stream(current)
+    return out
 
 
 def _fmt(fmt) -> int:
@@ -256,14 +265,14 @@ def _gemm_operands(f: int, A, a_scales, B, b_scales, C):
     return M, N, K
 
 
-def _outputs(device, q, q_shape, q_dtype, scales, s_shape, s_dtype=torch.float32):
-    """Allocate the codes / scales outputs, or check the caller's."""
+def _outputs(like, stream, q, q_shape, q_dtype, scales, s_shape, s_dtype=torch.float32):
+    """Allocate the codes / scales outputs of a call on `stream`, or check the caller's."""
     if q is None:
-        q = torch.empty(q_shape, dtype=q_dtype, device=device)
+        q = _alloc(like, q_shape, stream, q_dtype)
     else:
         _need(q, "q", _CODE_DTYPES, len(q_shape), q_shape)
     if scales is None:
-        scales = torch.empty(s_shape, dtype=s_dtype, device=device)
+        scales = _alloc(like, s_shape, stream, s_dtype)
     else:
         _need(scales, "scales", (s_dtype,), len(s_shape), s_shape)
     return q, scales
@@ -279,7 +288,7 @@ def scaled_mm(fmt, A: torch.Tensor, a_scales: torch.Tensor, B: torch.Tensor, b_s
     f = _fmt(fmt)
     M, N, K = _gemm_operands(f, A, a_scales, B, b_scales, C)
     if C is None:
-        C = torch.empty((M, N), dtype=torch.bfloat16, device=A.device)
+        C = _alloc(A, (M, N), stream, torch.bfloat16)
     rc = lib().lq_scaled_mm(f, _ptr(A), _ptr(a_scales), _ptr(B), _ptr(b_scales), _ptr(C), M, N, K,
                             ctypes.byref(variant) if variant is not None else None, _stream(stream))
     _check("lq_scaled_mm", rc)
@@ -299,9 +308,9 @@ def quant_scaled_mm(fmt, x: torch.Tensor, B: torch.Tensor, b_scales: torch.Tenso
         raise ValueError("x and B disagree on K")
     _need(b_scales, "b_scales", (torch.float32,), 1, (N,))
     if C is None:
-        C = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
+        C = _alloc(x, (M, N), stream, torch.bfloat16)
     _need(C, "C", (torch.bfloat16,), 2, (M, N))
-    q, s = _outputs(x.device, q, (M, K), _code_dtype(f), s, (M,))
+    q, s = _outputs(x, stream, q, (M, K), _code_dtype(f), s, (M,))
     _one_device(x, B, b_scales, C, q, s)
     rc = lib().lq_quant_scaled_mm(f, _ptr(x), _ptr(B), _ptr(b_scales), _ptr(C), _ptr(q), _ptr(s), M, N, K,
                                   ctypes.byref(variant) if variant is not None else None, _stream(stream))
@@ -318,7 +327,7 @@ def scaled_mm_bias(fmt, A: torch.Tensor, a_scales: torch.Tensor, B: torch.Tensor
     _need(bias, "bias", (torch.bfloat16,), 1, (N,))
     _one_device(A, bias)
     if C is None:
-        C = torch.empty((M, N), dtype=torch.bfloat16, device=A.device)
+        C = _alloc(A, (M, N), stream, torch.bfloat16)
     rc = lib().lq_scaled_mm_bias(f, _ptr(A), _ptr(a_scales), _ptr(B), _ptr(b_scales), _ptr(bias), _ptr(C), M, N, K,
                                  ctypes.byref(variant) if variant is not None else None, _stream(stream))
     _check("lq_scaled_mm_bias", rc)
@@ -342,7 +351,7 @@ def grouped_scaled_mm(fmt, A: torch.Tensor, a_scales: torch.Tensor, B: torch.Ten
     _need(b_scales, "b_scales", (torch.float32,), 2, (E, N))
     _need(expert_offsets, "expert_offsets", (torch.int32,), 1, (E + 1,))
     if C is None:
-        C = torch.empty((T, N), dtype=torch.bfloat16, device=A.device)
+        C = _alloc(A, (T, N), stream, torch.bfloat16)
     _need(C, "C", (torch.bfloat16,), 2, (T, N))
     _one_device(A, a_scales, B, b_scales, expert_offsets, C)
     rc = lib().lq_grouped_scaled_mm(f, _ptr(A), _ptr(a_scales), _ptr(B), _ptr(b_scales), _ptr(C),
@@ -359,7 +368,7 @@ def scaled_mm_noalloc(fmt, A: torch.Tensor, a_scales: torch.Tensor, B: torch.Ten
     f = _fmt(fmt)
     M, N, K = _gemm_operands(f, A, a_scales, B, b_scales, C)
     if C is None:
-        C = torch.empty((M, N), dtype=torch.bfloat16, device=A.device)
+        C = _alloc(A, (M, N), stream, torch.bfloat16)
     rc = lib().lq_scaled_mm_noalloc(f, _ptr(A), _ptr(a_scales), _ptr(B), _ptr(b_scales), _ptr(C), M, N, K,
                                     ctypes.byref(variant) if variant is not None else None, _stream(stream))
     _check("lq_scaled_mm_noalloc", rc)
@@ -372,9 +381,9 @@ def scaled_mm_i32acc(A, a_scales, B, b_scales, C=None, acc=None, variant: Varian
     _need(B, "B", (torch.int8,), 2)
     M, N, K = _gemm_operands(W8A8_INT8, A, a_scales, B, b_scales, C)
     if C is None:
-        C = torch.empty((M, N), dtype=torch.bfloat16, device=A.device)
+        C = _alloc(A, (M, N), stream, torch.bfloat16)
     if acc is None:
-        acc = torch.empty((M, N), dtype=torch.int32, device=A.device)
+        acc = _alloc(A, (M, N), stream, torch.int32)
     _need(acc, "acc", (torch.int32,), 2, (M, N))
     _one_device(A, acc)
     rc = lib().lq_scaled_mm_i32acc(_ptr(A), _ptr(a_scales), _ptr(B), _ptr(b_scales), _ptr(C), _ptr(acc), M, N, K,
@@ -389,7 +398,7 @@ def quant_per_token(fmt, x: torch.Tensor, q: torch.Tensor | None = None, scales:
     f = _fmt(fmt)
     _need(x, "x", (torch.bfloat16,), 2)
     M, K = x.shape
-    q, scales = _outputs(x.device, q, (M, K), _code_dtype(f), scales, (M,))
+    q, scales = _outputs(x, stream, q, (M, K), _code_dtype(f), scales, (M,))
     _one_device(x, q, scales)
     rc = lib().lq_quant_per_token(f, _ptr(x), _ptr(q), _ptr(scales), M, K, _stream(stream))
     _check("lq_quant_per_token", rc)
@@ -400,15 +409,15 @@ def quant_per_token_group128(x: torch.Tensor, q=None, scales=None, stream=None):
     """(e4m3 codes [M, K], scales [M, K/128]) of a bf16 [M, K] tensor."""
     _need(x, "x", (torch.bfloat16,), 2)
     M, K = x.shape
-    q, scales = _outputs(x.device, q, (M, K), torch.uint8, scales, (M, max(K // 128, 0)))
+    q, scales = _outputs(x, stream, q, (M, K), torch.uint8, scales, (M, max(K // 128, 0)))
     _one_device(x, q, scales)
     rc = lib().lq_quant_per_token_group128(_ptr(x), _ptr(q), _ptr(scales), M, K, _stream(stream))
     _check("lq_quant_per_token_group128", rc)
     return q, scales
 
 
-def _producer_out(f: int, M: int, K: int, per_block: bool, device, q, scales):
-    return _outputs(device, q, (M, K), _code_dtype(f), scales, (M, max(K // 128, 0)) if per_block else (M,))
+def _producer_out(f: int, M: int, K: int, per_block: bool, like, stream, q, scales):
+    return _outputs(like, stream, q, (M, K), _code_dtype(f), scales, (M, max(K // 128, 0)) if per_block else (M,))
 
 
 def _rms_inputs(x, weight, residual):
@@ -426,7 +435,7 @@ def rms_norm_dynamic_per_token_quant(fmt, x: torch.Tensor, weight: torch.Tensor,
     residual, when given, is overwritten with x + residual."""
     f = _fmt(fmt)
     M, K = _rms_inputs(x, weight, residual)
-    q, scales = _producer_out(f, M, K, False, x.device, q, scales)
+    q, scales = _producer_out(f, M, K, False, x, stream, q, scales)
     _one_device(x, weight, residual, q, scales)
     rc = lib().lq_rms_norm_dynamic_per_token_quant(f, _ptr(x), _ptr(residual) if residual is not None else None,
                                                    _ptr(weight), float(eps), _ptr(q), _ptr(scales), M, K,
@@ -439,7 +448,7 @@ def rms_norm_per_block_quant(x: torch.Tensor, weight: torch.Tensor, eps: float, 
                              scales=None, stream=None):
     """(e4m3 codes [M, K], scales [M, K/128]) of RMSNorm(x [+ residual]) * weight."""
     M, K = _rms_inputs(x, weight, residual)
-    q, scales = _producer_out(FP8_DYNAMIC, M, K, True, x.device, q, scales)
+    q, scales = _producer_out(FP8_DYNAMIC, M, K, True, x, stream, q, scales)
     _one_device(x, weight, residual, q, scales)
     rc = lib().lq_rms_norm_per_block_quant(_ptr(x), _ptr(residual) if residual is not None else None, _ptr(weight),
                                            float(eps), _ptr(q), _ptr(scales), M, K, _stream(stream))
@@ -459,7 +468,7 @@ def silu_and_mul_dynamic_per_token_quant(fmt, gate_up: torch.Tensor, q=None, sca
     """(codes [M, I], scales [M]) of silu(gate_up[:, :I]) * gate_up[:, I:]."""
     f = _fmt(fmt)
     M, I = _gate_up_width(gate_up)
-    q, scales = _producer_out(f, M, I, False, gate_up.device, q, scales)
+    q, scales = _producer_out(f, M, I, False, gate_up, stream, q, scales)
     _one_device(gate_up, q, scales)
     rc = lib().lq_silu_and_mul_dynamic_per_token_quant(f, _ptr(gate_up), _ptr(q), _ptr(scales), M, I,
                                                        _stream(stream))
@@ -470,7 +479,7 @@ def silu_and_mul_dynamic_per_token_quant(fmt, gate_up: torch.Tensor, q=None, sca
 def silu_and_mul_per_block_quant(gate_up: torch.Tensor, q=None, scales=None, stream=None):
     """(e4m3 codes [M, I], scales [M, I/128]) of silu(g) * u."""
     M, I = _gate_up_width(gate_up)
-    q, scales = _producer_out(FP8_DYNAMIC, M, I, True, gate_up.device, q, scales)
+    q, scales = _producer_out(FP8_DYNAMIC, M, I, True, gate_up, stream, q, scales)
     _one_device(gate_up, q, scales)
     rc = lib().lq_silu_and_mul_per_block_quant(_ptr(gate_up), _ptr(q), _ptr(scales), M, I, _stream(stream))
     _check("lq_silu_and_mul_per_block_quant", rc)
@@ -481,7 +490,7 @@ def quant_per_token_group128_ue8m0(x: torch.Tensor, q=None, scales=None, stream=
     """(e4m3 codes [M, K], UE8M0 scale bytes [M, K/128]) of a bf16 [M, K] tensor."""
     _need(x, "x", (torch.bfloat16,), 2)
     M, K = x.shape
-    q, scales = _outputs(x.device, q, (M, K), torch.uint8, scales, (M, max(K // 128, 0)), torch.uint8)
+    q, scales = _outputs(x, stream, q, (M, K), torch.uint8, scales, (M, max(K // 128, 0)), torch.uint8)
     _one_device(x, q, scales)
     rc = lib().lq_quant_per_token_group128_ue8m0(_ptr(x), _ptr(q), _ptr(scales), M, K, _stream(stream))
     _check("lq_quant_per_token_group128_ue8m0", rc)
@@ -492,7 +501,7 @@ def quant_weight_block128_ue8m0(w: torch.Tensor, q=None, scales=None, stream=Non
     """(e4m3 codes [N, K], UE8M0 scale bytes [N/128, K/128]) of a bf16 weight [N, K]."""
     _need(w, "w", (torch.bfloat16,), 2)
     N, K = w.shape
-    q, scales = _outputs(w.device, q, (N, K), torch.uint8, scales, (max(N // 128, 0), max(K // 128, 0)),
+    q, scales = _outputs(w, stream, q, (N, K), torch.uint8, scales, (max(N // 128, 0), max(K // 128, 0)),
                          torch.uint8)
     _one_device(w, q, scales)
     rc = lib().lq_quant_weight_block128_ue8m0(_ptr(w), _ptr(q), _ptr(scales), N, K, _stream(stream))
@@ -504,7 +513,7 @@ def quant_weight_block128(w: torch.Tensor, q=None, scales=None, stream=None):
     """(e4m3 codes [N, K], scales [N/128, K/128]) of a bf16 weight [N, K]."""
     _need(w, "w", (torch.bfloat16,), 2)
     N, K = w.shape
-    q, scales = _outputs(w.device, q, (N, K), torch.uint8, scales, (max(N // 128, 0), max(K // 128, 0)))
+    q, scales = _outputs(w, stream, q, (N, K), torch.uint8, scales, (max(N // 128, 0), max(K // 128, 0)))
     _one_device(w, q, scales)
     rc = lib().lq_quant_weight_block128(_ptr(w), _ptr(q), _ptr(scales), N, K, _stream(stream))
     _check("lq_quant_weight_block128", rc)
@@ -523,11 +532,11 @@ def quant_weight_int4(w: torch.Tensor, group: int = 128, zero_points: bool = Fal
     N, K = w.shape
     if group not in INT4_GROUPS or K % group:
         raise ValueError(f"group must be one of {INT4_GROUPS} and divide K = {K}, got {group}")
-    q, scales = _outputs(w.device, q, (N, K // 2), torch.uint8, scales, (N, K // group), torch.bfloat16)
+    q, scales = _outputs(w, stream, q, (N, K // 2), torch.uint8, scales, (N, K // group), torch.bfloat16)
     if zeros is not None:
         _need(zeros, "zeros", (torch.uint8,), 2, (N, K // group))
     elif zero_points:
-        zeros = torch.empty((N, K // group), dtype=torch.uint8, device=w.device)
+        zeros = _alloc(w, (N, K // group), stream, torch.uint8)
     _one_device(w, q, scales, zeros)
     _check("lq_quant_weight_int4", lib().lq_quant_weight_int4(_ptr(w), group, _ptr(q), _ptr(scales), _ptr(zeros), N, K,
                                                               _stream(stream)))
@@ -565,7 +574,7 @@ def int4_mm(x: torch.Tensor, B: torch.Tensor, b_scales: torch.Tensor, b_zeros: t
     if bias is not None:
         _need(bias, "bias", (torch.bfloat16,), 1, (N,))
     if C is None:
-        C = x.new_empty((M, N))
+        C = _alloc(x, (M, N), stream)
     else:
         _need(C, "C", (torch.bfloat16,), 2, (M, N))
     _one_device(x, B, b_scales, b_zeros, bias, C)
@@ -586,7 +595,7 @@ def grouped_int4_mm(x: torch.Tensor, B: torch.Tensor, b_scales: torch.Tensor, ex
     T, N, K, group = _int4_operands(x, B, b_scales, b_zeros, (E,))
     _need(expert_offsets, "expert_offsets", (torch.int32,), 1, (E + 1,))
     if C is None:
-        C = x.new_empty((T, N))
+        C = _alloc(x, (T, N), stream)
     else:
         _need(C, "C", (torch.bfloat16,), 2, (T, N))
     _one_device(x, B, b_scales, b_zeros, expert_offsets, C)
@@ -603,7 +612,7 @@ def moe_sort(topk_ids: torch.Tensor, num_experts: int, expert_offsets=None, orde
     T, k = topk_ids.shape
     E, n = int(num_experts), T * k
     if expert_offsets is None and order is None and slots is None and E >= 0:   # one allocation, cut in three
-        buf = topk_ids.new_empty(E + 1 + 2 * n, dtype=torch.int32)
+        buf = _alloc(topk_ids, (E + 1 + 2 * n,), stream, torch.int32)
         offs, rows, cut = torch.unsafe_split_with_sizes(buf, (E + 1, n, n))
         outs = (offs, rows, cut.view(T, k))
         _one_device(topk_ids)
@@ -612,7 +621,7 @@ def moe_sort(topk_ids: torch.Tensor, num_experts: int, expert_offsets=None, orde
         for name, t, shape in (("expert_offsets", expert_offsets, (E + 1,)), ("order", order, (n,)),
                                ("slots", slots, (T, k))):
             if t is None:
-                t = topk_ids.new_empty(shape, dtype=torch.int32)
+                t = _alloc(topk_ids, shape, stream, torch.int32)
             else:
                 _need(t, name, (torch.int32,), len(shape), shape)
             outs.append(t)
@@ -637,7 +646,7 @@ def moe_permute(x: torch.Tensor, slots: torch.Tensor, xs: torch.Tensor | None = 
     T, H = x.shape
     k = _token_slots(slots, T)
     if xs is None:
-        xs = x.new_empty((T * k, H))
+        xs = _alloc(x, (T * k, H), stream)
     else:
         _need(xs, "xs", (torch.bfloat16,), 2, (xs.shape[0], H))
     _one_device(x, slots, xs)
@@ -658,7 +667,7 @@ def moe_permute_quant(fmt, x: torch.Tensor, slots: torch.Tensor, q: torch.Tensor
     if q is not None and q.dim() != 2:
         raise ValueError("q must be a contiguous 2-d tensor")
     P = T * k if q is None else q.shape[0]
-    q, scales = _outputs(x.device, q, (P, H), _code_dtype(f), scales, (P,))
+    q, scales = _outputs(x, stream, q, (P, H), _code_dtype(f), scales, (P,))
     _one_device(x, slots, q, scales)
     _check("lq_moe_permute_quant", lib().lq_moe_permute_quant(f, _ptr(x), _ptr(slots), _ptr(q), _ptr(scales), T, P, k,
                                                               H, _stream(stream)))
@@ -677,7 +686,7 @@ def moe_unpermute(y: torch.Tensor, slots: torch.Tensor, weights: torch.Tensor | 
     if weights is not None:
         _need(weights, "weights", (torch.float32,), 2, (T, k))
     if out is None:
-        out = y.new_empty((T, H))
+        out = _alloc(y, (T, H), stream)
     else:
         _need(out, "out", (torch.bfloat16,), 2, (T, H))
     _one_device(y, slots, weights, out)
@@ -706,11 +715,11 @@ def moe_unpermute_backward(dout: torch.Tensor, y: torch.Tensor, slots: torch.Ten
     _need(dout, "dout", (torch.bfloat16,), 2, (T, H))
     _need(weights, "weights", (torch.float32,), 2, (T, k))
     if dy is None:
-        dy = _zeros(y, (P, H), stream)
+        dy = _alloc(y, (P, H), stream, zero=True)
     else:
         _need(dy, "dy", (torch.bfloat16,), 2, (P, H))
     if dweights is None:
-        dweights = weights.new_empty((T, k))
+        dweights = _alloc(weights, (T, k), stream)
     else:
         _need(dweights, "dweights", (torch.float32,), 2, (T, k))
     _one_device(dout, y, slots, weights, dy, dweights)
@@ -784,7 +793,7 @@ def test_silu_bf16(gate: torch.Tensor, stream=None) -> torch.Tensor:
     """Test hook: bf16(silu(gate)) by the producer kernels' own device code."""
     if gate.dtype != torch.bfloat16 or not gate.is_cuda or not gate.is_contiguous():
         raise ValueError("gate must be a contiguous bf16 CUDA tensor")
-    out = torch.empty_like(gate)
+    out = _alloc(gate, gate.shape, stream)
     _check("lq_test_silu_bf16", lib().lq_test_silu_bf16(_ptr(gate), _ptr(out), gate.numel(), _stream(stream)))
     return out
 

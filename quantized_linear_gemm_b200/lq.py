@@ -589,7 +589,9 @@ def grouped_int4_mm(x: torch.Tensor, B: torch.Tensor, b_scales: torch.Tensor, ex
     packed codes, b_scales (and b_zeros) [E, N, K/group], expert_offsets int32
     [E + 1] on the device.  Returns C [T, N] bf16; rows outside every expert
     are left as they were."""
-    if not isinstance(B, torch.Tensor) or B.dim() != 3:
+    if not isinstance(B, torch.Tensor):
+        raise TypeError("B must be a tensor")
+    if B.dim() != 3:
         raise ValueError("B must be a contiguous 3-d tensor [E, N, K / 2]")
     E = B.shape[0]
     T, N, K, group = _int4_operands(x, B, b_scales, b_zeros, (E,))
@@ -648,7 +650,9 @@ def moe_permute(x: torch.Tensor, slots: torch.Tensor, xs: torch.Tensor | None = 
     if xs is None:
         xs = _alloc(x, (T * k, H), stream)
     else:
-        _need(xs, "xs", (torch.bfloat16,), 2, (xs.shape[0], H))
+        _need(xs, "xs", (torch.bfloat16,), 2)
+        if xs.shape[1] != H:
+            raise ValueError(f"xs has rows of {xs.shape[1]} values, expected {H}")
     _one_device(x, slots, xs)
     _check("lq_moe_permute", lib().lq_moe_permute(_ptr(x), _ptr(slots), _ptr(xs), T, xs.shape[0], k, H,
                                                   _stream(stream)))
@@ -664,8 +668,8 @@ def moe_permute_quant(fmt, x: torch.Tensor, slots: torch.Tensor, q: torch.Tensor
     _need(x, "x", (torch.bfloat16,), 2)
     T, H = x.shape
     k = _token_slots(slots, T)
-    if q is not None and q.dim() != 2:
-        raise ValueError("q must be a contiguous 2-d tensor")
+    if q is not None:
+        _need(q, "q", _CODE_DTYPES, 2)
     P = T * k if q is None else q.shape[0]
     q, scales = _outputs(x, stream, q, (P, H), _code_dtype(f), scales, (P,))
     _one_device(x, slots, q, scales)

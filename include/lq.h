@@ -487,13 +487,15 @@ lq_status lq_quant_weight_int4(const void *w, int64_t group, void *q, void *scal
  *   K        : a positive multiple of group, at most 2^24; N % 8 == 0;
  *              M < 2^31 - 255.
  *              M == 0 or N == 0 is a no-op.
- * Up to 8 tokens (16 rows of a grouped call) the codes minus the zero points
- * are exact, a group's products are summed in fp32 and then multiplied by the
- * group's scale in fp32; for more tokens, and for few tokens of long or
- * finely grouped rows, the weight (q - z) s is rounded once to bf16 and
- * multiplied on the tensor core with fp32 sums.  |b_scales| < 2^34; weights below
- * 2^-86 and sums below 2^-60 in magnitude may lose precision.  No workspace: calls on different
- * streams may overlap.  Reads B only after the previous kernels on the stream
+ * Up to 8 tokens the codes minus the zero points are exact, a group's products
+ * are summed in fp32 and then multiplied by the group's scale in fp32.  For more
+ * tokens, and for few tokens with K > 16384 or with group 64 and N >= 16384, the
+ * weight (q - z) s is rounded once to bf16 (a relative error of at most 2^-8) and
+ * multiplied on the tensor core with fp32 sums: a token's row may therefore
+ * differ in its last bits between a batch of 8 and one of 9 tokens.  Scales that
+ * are powers of two make that rounding exact.  |b_scales| < 2^34; weights below
+ * 2^-86 and sums below 2^-60 in magnitude may lose precision.  No workspace:
+ * calls on different streams may overlap.  Reads B only after the previous kernels on the stream
  * have finished unless lq_declare_static_weights(1) was called.
  * Errors: LQ_ERR_INVALID_ARG, LQ_ERR_ALIGNMENT, LQ_ERR_UNSUPPORTED_SHAPE
  * before any launch; LQ_ERR_WORKSPACE when the device has not been initialised
@@ -509,7 +511,9 @@ lq_status lq_int4_mm(const void *x, const void *B, const void *b_scales,
  * expert_offsets as for lq_grouped_scaled_mm (clamped to [0, T] and to their
  * running maximum; the last may be below T); rows of C outside every expert are
  * left as they were, and rows of x outside every expert do not matter.
- * E * N < 2^31.  Errors as lq_int4_mm; LQ_ERR_INVALID_ARG for E = 0 with T > 0.
+ * The weights are exact (lq_int4_mm) up to 16 rows (8 for E = 1) and for E > 1024,
+ * else rounded once to bf16; E > 1024 reads an expert's weight once per 8 or 16 of its
+ * rows.  E * N < 2^31.  Errors as lq_int4_mm; LQ_ERR_INVALID_ARG for E = 0 with T > 0.
  */
 lq_status lq_grouped_int4_mm(const void *x, const void *B, const void *b_scales,
                              const void *b_zeros, void *C, const int32_t *expert_offsets,
@@ -529,15 +533,15 @@ lq_status lq_grouped_int4_mm(const void *x, const void *B, const void *b_scales,
  *            expert_offsets[e + 1] - 1, as the grouped products read them.
  *   order  : [n] out: order[p] = i, the pair of row p; -1 behind the last row.
  *   slots  : [n] out: slots[i] = p, the row of pair i, or -1.
- *   1 <= E <= 1024, n < 2^31.  n == 0 writes zero offsets.  One launch; no
+ *   1 <= E <= 1024, n < 2^31; no array overlaps another.  n == 0 writes zero offsets.  One launch; no
  *   workspace, no atomics.
  *
  * In the calls below T tokens have k slots each (slots [T, k], from
  * lq_moe_sort), P is the number of rows of the sorted arrays (T * k, or fewer
  * when the caller knows a bound), and a slot outside [0, P) is skipped: its
  * row is neither read nor written.  Rows that no slot names are left as they
- * were.  Slots that name a row twice give that row one of the two values.
- * Outputs must not overlap inputs.  H % 8 == 0 (lq_moe_permute_quant: 16), H <= 2^25,
+ * were.  A row that two slots name gets pieces of both of its values (codes and
+ * scale too); reading one twice is fine.  Outputs must not overlap inputs.  H % 8 == 0 (lq_moe_permute_quant: 16), H <= 2^25,
  * k <= 2^24; rows are dense and 16-byte aligned (codes 8).
  *
  * lq_moe_permute: xs[slots[t, j]] = x[t]; x [T, H] bf16, xs [P, H] bf16.  Its

@@ -32,9 +32,11 @@ namespace {
 // quotient is the correctly rounded fp32 one and rint rounds half to even;
 // the codes are those of the bf16 scale that is stored.
 //
-// Run once per weight.  Bound by the issue of eight correctly rounded divisions
-// per thread, not by HBM: [24576, 4096], G = 128, 84 us (3.0 TB/s, 0.46 of the
-// copy rate), with zero points 90 us; [4096, 4096] 15 us.
+// Run once per weight.  Held back by the issue of eight correctly rounded
+// divisions per thread, not by HBM: [24576, 4096], G = 128, 84 us (3.0 TB/s,
+// 0.46 of the copy rate), with zero points 90 us; [4096, 4096] 15 us.  That is no
+// floor: one reciprocal per group and corrected products (quotient8) would give
+// the same quotients with fewer instructions.
 template <int G, bool kZeros>
 __global__ void __launch_bounds__(256) quant_weight_int4_kernel(const uint4* __restrict__ w,
                                                                 uint32_t* __restrict__ q,

@@ -27,8 +27,8 @@
 // weights every 400 cycles, with one CTA as with two, where HBM alone needs
 // 370; what remains is the launch, the first block's way through the roles and
 // the last, partly filled round of tiles.  [37888, 4096], 16 tokens: 16.8 us,
-// 4.7 TB/s, 0.72 of the copy rate; [5120, 25600], 37 tokens: 26 us, 0.41 (seven
-// CTAs share a tile's K).  Many tokens: the tensor core, and the converting
+// 4.7 TB/s, 0.72 of the copy rate; [5120, 25600], 37 tokens: 25.4 us, 0.42 (six
+// CTAs share a tile's K: 240 on 148 SMs, so the SMs with two of them set the time).  Many tokens: the tensor core, and the converting
 // warps that compete with it for power and issue slots: [24576, 4096], 2048
 // tokens, 321 to 335 us, 1.23 to 1.29 PFLOP/s, 0.73 to 0.76 of the burst rate of
 // a bf16 library product (0.89 of the sustained one).  Several accumulators per
@@ -622,11 +622,11 @@ cudaError_t launch_mma_gn(const Int4Params& params, cudaStream_t stream) {
   cfg.stream = stream;
 
   // Split-K: few tiles, each shared by a cluster of as many CTAs as find an SM
-  // of their own and keep at least 8 blocks each; two per SM only where that
-  // leaves them 48 blocks or more.  Measured on B200, us with splits 1..8:
+  // of their own and keep at least 8 blocks each; as many as fit two per SM where
+  // those with an SM of their own would have 48 blocks or more.  Measured on B200, us with splits 1..8:
   // [4096, 4096], 16 tokens: 13.0 9.2 7.9 7.3 | 8.8 8.8 8.6 8.4 (two per SM from 5);
   // [4096, 12288], 64 tokens: 42.2 25.2 19.8 16.8 | 20.3 18.8 18.8 18.6;
-  // [5120, 25600], 64 tokens: 86.9 47.9 34.6 | 35.7 31.4 28.3 44.5 40.6 (7 and 8 do not fit).
+  // [5120, 25600], 64 tokens: 86.9 47.9 34.6 | 35.7 31.4 28.3 44.5 40.6 (7 and 8 do not fit; 6 is taken, 33 blocks each).
   p.split = 1;
   static std::atomic<int> room[2][64][kMaxSplit + 1];
   if (!p.expert_offsets && tiles <= 148) {

@@ -19,7 +19,8 @@ struct MmaShape {
   static constexpr int kStage = kWeightTile + kTokenTile;
   static constexpr bool kTwo = NT <= 64;
   // converting groups of four warps, group g takes blocks g, g + kGroups, ...; one keeps up with the
-  // MMAs of 256 tokens, and with 14 warps the epilogue has the registers for its packed columns
+  // MMAs of 256 tokens, and 14 warps have 128 registers a thread (18 have 96), so that the epilogue's 64
+  // words of packed columns spill 92 to 120 bytes only
   static constexpr int kGroups = NT == 256 ? 1 : 2;
   // converted weight blocks in tensor memory.  128 tokens: with four, a ring of five slots does not meet
   // the condition below; three and five, or four and a ring of four: [24576, 4096] at 128 tokens 32.2 / 35.0 us,

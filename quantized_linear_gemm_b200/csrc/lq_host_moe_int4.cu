@@ -26,12 +26,21 @@ bool group_ok(int64_t group) { return group == 32 || group == 64 || group == 128
 // Measured on B200, us (streaming / tensor core).  Dense, G = 128: 1 token
 // [4096, 4096] 4.7 / 7.3, [24576, 4096] 15.5 / 19, [4096, 12288] 9.9 / 12.4,
 // [5120, 25600] 32.8 / 21.5; 16 tokens 10.2 / 7.0, 27.3 / 22, 23.1 / 12.4,
-// 66.5 / 22.  G = 64, [24576, 4096], 8 tokens 25 / 20.5 (the streaming kernel
-// loads 8 bytes at a time there).
+// 66.5 / 22.  G = 64 (the streaming kernel loads 8 bytes at a time there):
+// [24576, 4096] 1 token 24.3 / 21.3, 8 tokens 25.2 / 21.3, with zero points
+// 31.1 / 25.2 and 32.3 / 24.8; [16384, 4096] 1 token 16.7 / 15.3; [12288, 4096]
+// 1 token 12.9 / 15.1, 8 tokens 14.1 / 15.1.
 // Grouped, 128 experts, [1536, 2048] each: 8 rows 7.1 / 10.6, 64 rows 35 / 29,
-// 512 rows 86 / 56.  Its tile covers one and a half times the average expert:
-// 2048 rows 75, 59, 64 us with tiles of 16, 32, 64; 32768 rows [2048, 768]
-// 204, 156, 175 us with 64, 128, 256.
+// 512 rows 86 / 56.  More experts than the tensor-core kernel keeps take the
+// streaming kernel at any number of rows.
+//
+// A grouped tile covers one and a half times the average expert, since the
+// offsets are on the device.  [1536, 2048], evenly routed: 256 rows 51, 55, 56 us
+// with tiles of 16, 32, 64; 8008 rows 127, 88, 89, 123 with 32, 64, 128, 256;
+// 32768 rows 266, 227, 214 with 64, 128, 256.  With half of the rows on four
+// experts, or very uneven shares, the rule's tile is at most 17 % behind the best
+// one: 1024 rows 66.0 (64.2 with 32) and 54.3 (46.3 with 32), 8008 rows 101
+// (92.3 with 64) and 89.2 (the best), 32768 rows 230 (221 with 256) and 229 (222).
 int tensor_tile(int64_t M, int64_t N, int64_t K, int64_t group, int64_t experts) {
   if (experts) {
     if (M <= (experts > 1 ? 16 : 8) || experts > lq::int4_mma_max_experts()) return 0;

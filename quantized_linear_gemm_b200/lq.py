@@ -3,8 +3,13 @@
 Every function here checks its tensors (dtype, rank, contiguity, the exact
 shape the C function reads or writes, and one device: the current CUDA
 device), then calls the C function of the same name in ``liblq.so`` on
-torch's current CUDA stream.  All arithmetic runs in the library's CUDA kernels; there is no
+torch's current CUDA stream, or on `stream`, whose memory the outputs then come
+from.  All arithmetic runs in the library's CUDA kernels; there is no
 fallback.  If ``liblq.so`` is missing the first call raises.
+
+No function takes part in autograd: an output carries no graph even when an
+input requires a gradient.  The gradients that the library has are functions of
+their own (moe_permute_backward, moe_unpermute_backward).
 """
 
 from __future__ import annotations
@@ -588,7 +593,7 @@ def grouped_int4_mm(x: torch.Tensor, B: torch.Tensor, b_scales: torch.Tensor, ex
     """``lq_grouped_int4_mm``: x [T, K] bf16 sorted by expert, B [E, N, K/2]
     packed codes, b_scales (and b_zeros) [E, N, K/group], expert_offsets int32
     [E + 1] on the device.  Returns C [T, N] bf16; rows outside every expert
-    are left as they were."""
+    are left as they were, which in a C allocated here is undefined."""
     if not isinstance(B, torch.Tensor):
         raise TypeError("B must be a tensor")
     if B.dim() != 3:
@@ -643,7 +648,7 @@ def _token_slots(slots, T: int) -> int:
 def moe_permute(x: torch.Tensor, slots: torch.Tensor, xs: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """``lq_moe_permute``: xs[slots[t, j]] = x[t] for bf16 x [T, H] and slots
     int32 [T, k].  xs [P, H] (default P = T * k); rows that no slot names are
-    left as they were."""
+    left as they were, which in an xs allocated here is undefined."""
     _need(x, "x", (torch.bfloat16,), 2)
     T, H = x.shape
     k = _token_slots(slots, T)
@@ -663,7 +668,8 @@ def moe_permute_quant(fmt, x: torch.Tensor, slots: torch.Tensor, q: torch.Tensor
                       scales: torch.Tensor | None = None, stream=None):
     """``lq_moe_permute_quant``: (codes [P, H], scales fp32 [P]) of x [T, H]
     quantized per token (``fp8_dynamic`` or ``w8a8_int8``) and placed at its
-    slots; P = T * k unless q is given."""
+    slots; P = T * k unless q is given.  Rows that no slot names are left as
+    they were, which in outputs allocated here is undefined."""
     f = _fmt(fmt)
     _need(x, "x", (torch.bfloat16,), 2)
     T, H = x.shape
@@ -701,7 +707,8 @@ def moe_unpermute(y: torch.Tensor, slots: torch.Tensor, weights: torch.Tensor | 
 
 def moe_permute_backward(dxs: torch.Tensor, slots: torch.Tensor, dx: torch.Tensor | None = None,
                          stream=None) -> torch.Tensor:
-    """Gradient of moe_permute: dx[t] = sum_j dxs[slots[t, j]] (``lq_moe_unpermute`` without weights)."""
+    """Gradient of moe_permute: dx[t] = sum_j dxs[slots[t, j]]
+    (``lq_moe_unpermute`` without weights); rows without a slot are not read."""
     return moe_unpermute(dxs, slots, None, out=dx, stream=stream)
 
 

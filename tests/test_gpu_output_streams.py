@@ -98,3 +98,27 @@ def test_outputs_read_on_the_current_stream_are_not_handed_out_before(cuda_devic
             t.copy_(junk)
     torch.cuda.synchronize()
     assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("name", ["int4_mm", "moe_sort", "moe_unpermute_backward", "scaled_mm"])
+def test_captured_on_a_forked_stream(cuda_device, name):
+    """A call on a side stream that joins a capture, its outputs allocated inside it: replayed twice."""
+    call = operands()[name]
+    want = [t.clone() for t in listed(call())]
+    main, side = torch.cuda.Stream(), torch.cuda.Stream()
+    call(stream=side)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=main):
+        side.wait_stream(main)
+        out = listed(call(stream=side))
+        again = listed(call(stream=side))
+        main.wait_stream(side)
+    for _ in range(2):
+        for t in out + again:
+            t.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        for got in (out, again):
+            for a, b in zip(got, want):
+                assert np.array_equal(a.view(torch.uint8).cpu().numpy(), b.view(torch.uint8).cpu().numpy())

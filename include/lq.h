@@ -533,16 +533,17 @@ lq_status lq_grouped_int4_mm(const void *x, const void *B, const void *b_scales,
  *            expert_offsets[e + 1] - 1, as the grouped products read them.
  *   order  : [n] out: order[p] = i, the pair of row p; -1 behind the last row.
  *   slots  : [n] out: slots[i] = p, the row of pair i, or -1.
- *   1 <= E <= 1024, n < 2^31; no array overlaps another.  n == 0 writes zero offsets.  One launch; no
- *   workspace, no atomics.
+ *   1 <= E <= 1024, n < 2^31; no array overlaps another.  n == 0 writes zero
+ *   offsets.  One launch; no workspace, no atomics.
  *
  * In the calls below T tokens have k slots each (slots [T, k], from
  * lq_moe_sort), P is the number of rows of the sorted arrays (T * k, or fewer
  * when the caller knows a bound), and a slot outside [0, P) is skipped: its
  * row is neither read nor written.  Rows that no slot names are left as they
  * were.  A row that two slots name gets pieces of both of its values (codes and
- * scale too); reading one twice is fine.  Outputs must not overlap inputs.  H % 8 == 0 (lq_moe_permute_quant: 16), H <= 2^25,
- * k <= 2^24; rows are dense and 16-byte aligned (codes 8).
+ * scale too); reading one twice is fine.  Outputs must not overlap inputs.
+ * H % 8 == 0 (lq_moe_permute_quant: 16), H <= 2^25, k <= 2^24; rows are dense and
+ * 16-byte aligned (codes 8).
  *
  * lq_moe_permute: xs[slots[t, j]] = x[t]; x [T, H] bf16, xs [P, H] bf16.  Its
  *   gradient is lq_moe_unpermute with weights NULL.

@@ -318,10 +318,9 @@ cudaError_t launch_stream_gmr(const Int4Params& p, cudaStream_t stream) {
 // one token, G = 128: [4096, 4096] 4.7 us with 16 rows / 16 warps, 8.0 us with
 // 32 / 8; [4096, 12288] 9.8 and 20.0; [24576, 4096] 18.9 and 15.5.  An SM holds
 // two CTAs of 16 warps, so more than 296 row tiles take a second, partly filled
-// round: [6144, 4096], 384 tiles, 7.8 us.  Grouped:
-// the tiles of many experts are enough rows; two 8-token tiles per CTA where
-// the experts have more than 8 rows on average (more than 1024 experts: fewer
-// take the tensor-core kernel).
+// round: [6144, 4096], 384 tiles, 7.8 us.  Grouped: the tiles of many experts
+// are enough rows; two 8-token tiles per CTA where the experts have more than 8
+// rows on average (more than 1024 experts: fewer take the tensor-core kernel).
 template <int G>
 cudaError_t launch_stream_g(const Int4Params& p, cudaStream_t stream) {
   if (!p.expert_offsets)

@@ -26,12 +26,13 @@
 // What bounds it.  Few tokens: in steady state an SM takes a 128 x 128 block of
 // weights every 400 cycles, with one CTA as with two, where HBM alone needs
 // 370; what remains is the launch, the first block's way through the roles and
-// the last, partly filled round of tiles.  [37888, 4096], 16 tokens: 16.8 us,
-// 4.7 TB/s, 0.72 of the copy rate; [5120, 25600], 37 tokens: 25.4 us, 0.42 (six
-// CTAs share a tile's K: 240 on 148 SMs, so the SMs with two of them set the time).  Many tokens: the tensor core, and the converting
-// warps that compete with it for power and issue slots: [24576, 4096], 2048
-// tokens, 321 to 335 us, 1.23 to 1.29 PFLOP/s, 0.73 to 0.76 of the burst rate of
-// a bf16 library product (0.89 of the sustained one).  Several accumulators per
+// the last, partly filled round of tiles.  [37888, 4096], 16 tokens: 20.5 us,
+// 4.0 TB/s, 0.61 of the copy rate; [5120, 25600], 37 tokens: 25.3 us, 0.42 (six
+// CTAs share a tile's K: 240 on 148 SMs, so the SMs with two of them set the
+// time).  Many tokens: the tensor core, and the converting warps that compete
+// with it for power and issue slots: [24576, 4096], 2048 tokens, 321 to 335 us
+// call after call, 1.23 to 1.29 PFLOP/s, 0.73 to 0.76 of the burst rate of a bf16
+// library product (0.89 of the sustained one); 286 us in a short burst.  Several accumulators per
 // tile, or one MMA per block instead of eight, change nothing at few tokens.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -355,7 +356,7 @@ __global__ void __launch_bounds__(MmaShape<NT>::kThreads, MmaShape<NT>::kTwo ? 2
     };
     // of a block's groups, packed as they lie in memory and taken apart at their use: a load whose result
     // is unpacked where two ways of loading meet would be waited for there.  One load instead of one per
-    // group: [24576, 4096], 64 tokens, G = 32 with zero points 55 -> 33 us; [5120, 25600], 37 tokens, G = 64
+    // group: [24576, 4096], 64 tokens, G = 32 with zero points 55 -> 27 us; [5120, 25600], 37 tokens, G = 64
     // with zero points 35.7 -> 31.6 us.
     uint32_t s_next[(GB + 1) / 2], z_next = 0;
     auto load_scales = [&] {
@@ -623,10 +624,11 @@ cudaError_t launch_mma_gn(const Int4Params& params, cudaStream_t stream) {
 
   // Split-K: few tiles, each shared by a cluster of as many CTAs as find an SM
   // of their own and keep at least 8 blocks each; as many as fit two per SM where
-  // those with an SM of their own would have 48 blocks or more.  Measured on B200, us with splits 1..8:
+  // those with an SM of their own would have 48 blocks or more.  Measured on
+  // B200, us with splits 1..8:
   // [4096, 4096], 16 tokens: 13.0 9.2 7.9 7.3 | 8.8 8.8 8.6 8.4 (two per SM from 5);
   // [4096, 12288], 64 tokens: 42.2 25.2 19.8 16.8 | 20.3 18.8 18.8 18.6;
-  // [5120, 25600], 64 tokens: 86.9 47.9 34.6 | 35.7 31.4 28.3 44.5 40.6 (7 and 8 do not fit; 6 is taken, 33 blocks each).
+  // [5120, 25600], 64 tokens: 86.9 47.9 34.6 | 35.7 31.4 28.3 44.5 40.6 (7 and 8 do not fit; 6 it is).
   p.split = 1;
   static std::atomic<int> room[2][64][kMaxSplit + 1];
   if (!p.expert_offsets && tiles <= 148) {

@@ -127,7 +127,8 @@ def test_captured_on_a_forked_stream(cuda_device, name):
 def test_no_tokens_on_a_side_stream(cuda_device):
     """Empty outputs."""
     side = torch.cuda.Stream()
-    x, slots = torch.empty((0, 64), dtype=torch.bfloat16, device="cuda"), torch.empty((0, 2), dtype=torch.int32, device="cuda")
+    x = torch.empty((0, 64), dtype=torch.bfloat16, device="cuda")
+    slots = torch.empty((0, 2), dtype=torch.int32, device="cuda")
     assert lq.moe_permute(x, slots, stream=side).shape == (0, 64)
     assert lq.moe_unpermute(x, slots, stream=side).shape == (0, 64)
     off, order, got = lq.moe_sort(slots, 3, stream=side)
